@@ -9,6 +9,11 @@ entry points:
     dequantize(w)                        -> bf16 K x N    (qlora_nf4_dequantize)
     linear_forward(X, w, A, B, c)        -> (Y, Zc)       (qlora_linear_fwd)
     linear_backward(dY, X, Zc, w, A, B, c) -> (dX, dA, dB) (qlora_linear_bwd)
+    act8_quantize(X) -> Act8, act8_dequantize(a)          (qlora_act8_*)
+    gated_forward(X, wg, wu, Ag, Bg, Au, Bu, c) -> (H, saved)     (qlora_gated_fwd)
+    gated_backward(dH, X, saved, wg, wu, ...) -> (dX, dAg, dBg, dAu, dBu)
+    head_loss_forward(X, w, labels) -> (loss, lse)        (qlora_head_loss_fwd)
+    head_loss_backward(dloss, X, lse, w, labels) -> dX    (qlora_head_loss_bwd)
 
 Page "QLoRA：冻结的 4-bit 权重怎样参与一次微调" defines the method (see the
 header for the section of each call).
@@ -20,12 +25,18 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _lib
+from . import _args, _lib
 from ._lib import NF4StateC, QLoRAError, check, lib
+from .act8 import Act8, act8_dequantize, act8_quantize, check_act8
+from .gated import GatedSaved, gated_backward, gated_forward
+from .loss import head_loss_backward, head_loss_forward
 
 __all__ = ["NF4Weight", "quantize", "dequantize", "merge", "merge_requantize",
            "quantize_shard_begin", "quantize_shard_end", "shard_workspace_size",
            "linear_forward", "linear_backward",
+           "Act8", "act8_quantize", "act8_dequantize",
+           "GatedSaved", "gated_forward", "gated_backward",
+           "head_loss_forward", "head_loss_backward",
            "status_sync", "status_clear", "new_status", "QLoRAError", "lib"]
 
 BLOCKSIZE = 64
@@ -320,9 +331,13 @@ def linear_forward(X, w: NF4Weight, A, B, c: float, *, Y=None, Zc=None, status=N
 
 
 def linear_backward(dY, X, Zc, w: NF4Weight, A, B, c: float, *, dX=None, dA=None, dB=None,
-                    status=None, workspace=None):
+                    status=None, workspace=None, grad_dtype=torch.float32):
     """dX = dY·Ŵᵀ + c·(dY·Bᵀ)·Aᵀ, dA = Xᵀ·(c·dY·Bᵀ), dB = Zcᵀ·dY; returns (dX, dA, dB).
-    Zc=None recomputes bf16(c·X·A) inside the call (bit-identical to the forward's)."""
+    Zc=None recomputes bf16(c·X·A) inside the call (bit-identical to the forward's).
+    X may be the input's ``Act8`` (Zc is then needed); dA and dB are of
+    ``grad_dtype`` (fp32 or bf16)."""
+    if isinstance(X, Act8) or grad_dtype != torch.float32:
+        return _linear_backward_act8(dY, X, Zc, w, A, B, c, dX, dA, dB, status, workspace, grad_dtype)
     for t, n in ((dY, "dY"), (X, "X"), (A, "A"), (B, "B")):
         _bf16(t, n)
     if Zc is not None:
@@ -346,3 +361,44 @@ def linear_backward(dY, X, Zc, w: NF4Weight, A, B, c: float, *, dX=None, dA=None
           "qlora_linear_bwd")
     _finish(status, own, "qlora_linear_bwd")
     return dX, dA, dB
+
+
+def _linear_backward_act8(dY, X, Zc, w, A, B, c, dX, dA, dB, status, workspace, grad_dtype):
+    """linear_backward through qlora_linear_bwd_act8."""
+    M, N, dev = _args.cuda_2d(dY, "dY")
+    is8 = isinstance(X, Act8)
+    K = X.shape[1] if (is8 or isinstance(X, torch.Tensor)) and len(X.shape) == 2 else -1
+    if is8:
+        check_act8(X, "X", (M, K), dev)
+        if Zc is None:
+            raise ValueError("the backward from an 8-bit input needs the forward's Zc")
+    else:
+        _args.tensor(X, "X", (M, K), dev)
+    gcode = _args.grad_code(grad_dtype)
+    _args.weight(w, "w", (K, N), dev)
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise TypeError("A must be a matrix")
+    r = A.shape[1]
+    _args.tensor(A, "A", (K, r), dev)
+    _args.tensor(B, "B", (r, N), dev)
+    if Zc is not None:
+        _args.tensor(Zc, "Zc", (M, r), dev)
+    with torch.cuda.device(dev):
+        out = []
+        for t, name, shape, dt in ((dX, "dX", (M, K), torch.bfloat16), (dA, "dA", (K, r), grad_dtype),
+                                   (dB, "dB", (r, N), grad_dtype)):
+            if t is None:
+                t = torch.empty(shape, dtype=dt, device=dev)
+            else:
+                _args.tensor(t, name, shape, dev, dt)
+            out.append(t)
+        ws = _args.workspace(workspace, lib.qlora_linear_bwd_workspace_size(M, K, N, r), dev)
+        own = status is None
+        status = new_status(dev) if own else status
+        check(lib.qlora_linear_bwd_act8(M, K, N, r, dY.data_ptr(), None if is8 else X.data_ptr(),
+                                        C.byref(X.cstruct()) if is8 else None, _args.ptr(Zc),
+                                        C.byref(w.cstruct()), A.data_ptr(), B.data_ptr(), float(c),
+                                        *(t.data_ptr() for t in out), gcode, ws.data_ptr(), ws.numel(),
+                                        status.data_ptr(), _stream()), "qlora_linear_bwd_act8")
+        _finish(status, own, "qlora_linear_bwd_act8")
+    return tuple(out)

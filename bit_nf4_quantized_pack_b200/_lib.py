@@ -20,6 +20,8 @@ QLORA_ERR_CUDA = 5
 QLORA_ERR_TIMEOUT = 6
 QLORA_DTYPE_BF16 = 0
 QLORA_DTYPE_F32 = 1
+QLORA_ACT_SILU = 0
+QLORA_ACT_GELU = 1
 ABI_VERSION = 2
 NOALLOC_MAX_NUMEL = 1 << 26
 
@@ -40,9 +42,20 @@ class NF4StateC(C.Structure):
     ]
 
 
+class Act8C(C.Structure):
+    """Mirror of ``qlora_act8``."""
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("codes", C.c_void_p), ("scales", C.c_void_p)]
+
+
+class GatedSavedC(C.Structure):
+    """Mirror of ``qlora_gated_saved``."""
+    _fields_ = [(n, C.c_void_p) for n in ("G", "U", "G8", "U8", "G_scales", "U_scales", "Zg", "Zu")]
+
+
 # name -> (restype, argtypes): every symbol the header declares
 _VP, _I64, _I32, _SZ, _F = C.c_void_p, C.c_int64, C.c_int32, C.c_size_t, C.c_float
 _PS = C.POINTER(NF4StateC)
+_PA, _PG = C.POINTER(Act8C), C.POINTER(GatedSavedC)
 SIGNATURES = {
     "qlora_abi_version": (_I32, []),
     "qlora_status_str": (C.c_char_p, [_I32]),
@@ -64,6 +77,22 @@ SIGNATURES = {
     "qlora_linear_bwd_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
     "qlora_linear_bwd": (_I32, [_I64, _I64, _I64, _I32, _VP, _VP, _VP, _PS, _VP, _VP, _F,
                                 _VP, _VP, _VP, _VP, _SZ, _VP, _VP]),
+    "qlora_act8_quantize": (_I32, [_VP, _PA, _VP, _VP]),
+    "qlora_act8_dequantize": (_I32, [_PA, _VP, _VP]),
+    "qlora_linear_bwd_act8": (_I32, [_I64, _I64, _I64, _I32, _VP, _VP, _PA, _VP, _PS, _VP, _VP, _F,
+                                     _VP, _VP, _VP, _I32, _VP, _SZ, _VP, _VP]),
+    "qlora_gated_fwd_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
+    "qlora_gated_fwd": (_I32, [_I64, _I64, _I64, _I32, _VP, _PS, _PS, _VP, _VP, _VP, _VP, _F, _I32,
+                               _VP, _PG, _VP, _SZ, _VP, _VP]),
+    "qlora_gated_bwd_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
+    "qlora_gated_bwd": (_I32, [_I64, _I64, _I64, _I32, _VP, _VP, _PA, _PG, _PS, _PS, _VP, _VP, _VP,
+                               _VP, _F, _I32, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP, _VP]),
+    "qlora_head_loss_fwd_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "qlora_head_loss_fwd": (_I32, [_I64, _I64, _I64, _I64, _VP, _PS, _VP, _I64, _VP, _VP, _VP, _SZ,
+                                   _VP, _VP]),
+    "qlora_head_loss_bwd_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "qlora_head_loss_bwd": (_I32, [_I64, _I64, _I64, _I64, _VP, _VP, _VP, _PS, _VP, _I64, _VP, _VP,
+                                   _SZ, _VP, _VP]),
     "qlora_nf4_merge": (_I32, [_I64, _I64, _I32, _PS, _VP, _VP, _F, _VP, _VP, _VP]),
     "qlora_selftest_bounded_wait": (_I32, [_I64, _VP, _VP]),
     "qlora_profile_enable": (_I32, [_I32]),
@@ -74,6 +103,7 @@ SIGNATURES = {
 
 PROF_FUSED_FWD, PROF_FUSED_BWD, PROF_SKINNY, PROF_QUANTIZE = 0, 1, 2, 3
 PROF_DEQUANTIZE, PROF_GEMV, PROF_OTHER = 4, 5, 6
+PROF_ACT8, PROF_GATED, PROF_LOSS = 7, 8, 9
 
 
 def _load():

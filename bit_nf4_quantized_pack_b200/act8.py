@@ -1,0 +1,86 @@
+"""8-bit activation checkpoints (``qlora_act8_*`` in ``include/qlora_nf4.h``).
+
+A bf16 matrix that a layer keeps between its forward and its backward, in int8
+codes with one fp32 scale per 64 consecutive elements of a row: 1.0625 bytes an
+element instead of 2.  ``linear_backward`` and ``gated_backward`` take an
+``Act8`` in the place of their input and read the codes directly;
+``LinearChain(policy="int8")`` keeps every layer's input this way.
+"""
+from __future__ import annotations
+
+import ctypes as C
+from dataclasses import dataclass
+
+import torch
+
+from . import _args
+from ._lib import Act8C, check, lib
+
+__all__ = ["Act8", "act8_quantize", "act8_dequantize"]
+
+
+@dataclass
+class Act8:
+    """The checkpoint of an M x K matrix: ``codes`` int8 M x K and ``scales``
+    fp32 M x (K / 64)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @staticmethod
+    def empty(rows: int, cols: int, device="cuda") -> "Act8":
+        return Act8(torch.empty((rows, cols), dtype=torch.int8, device=device),
+                    torch.empty((rows, cols // 64), dtype=torch.float32, device=device))
+
+    def cstruct(self) -> Act8C:
+        return Act8C(self.codes.shape[0], self.codes.shape[1], self.codes.data_ptr(), self.scales.data_ptr())
+
+
+def check_act8(a, name, shape, dev):
+    """`a` is an Act8 of `shape` on `dev`, with buffers of the right extents."""
+    if not isinstance(a, Act8):
+        raise TypeError(f"{name} must be an Act8")
+    _args.tensor(a.codes, f"{name}.codes", shape, dev, torch.int8)
+    _args.tensor(a.scales, f"{name}.scales", (shape[0], shape[1] // 64), dev, torch.float32)
+
+
+def act8_quantize(X: torch.Tensor, *, out: Act8 | None = None, status: torch.Tensor | None = None) -> Act8:
+    """The 8-bit checkpoint of a contiguous CUDA bf16 matrix whose row length
+    is a multiple of 64.  A NaN or infinity in X is a device error."""
+    from . import _finish, new_status
+    M, K, dev = _args.cuda_2d(X, "X")
+    with torch.cuda.device(dev):
+        if out is None:
+            out = Act8.empty(M, K, dev)
+        else:
+            check_act8(out, "out", (M, K), dev)
+        own = status is None
+        status = new_status(dev) if own else status
+        st = out.cstruct()
+        check(lib.qlora_act8_quantize(X.data_ptr(), C.byref(st), status.data_ptr(), _args.stream()),
+              "qlora_act8_quantize")
+        _finish(status, own, "qlora_act8_quantize")
+    return out
+
+
+def act8_dequantize(a: Act8, *, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The bf16 matrix that the checkpoint stands for."""
+    if not isinstance(a, Act8) or not a.codes.is_cuda or a.codes.dim() != 2:
+        raise TypeError("a must be an Act8 on a CUDA device")
+    dev = a.device
+    check_act8(a, "a", tuple(a.codes.shape), dev)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty(a.codes.shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _args.tensor(out, "out", a.codes.shape, dev)
+        st = a.cstruct()
+        check(lib.qlora_act8_dequantize(C.byref(st), out.data_ptr(), _args.stream()), "qlora_act8_dequantize")
+    return out

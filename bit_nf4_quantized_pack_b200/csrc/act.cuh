@@ -1,0 +1,78 @@
+// Device arithmetic shared by the gated block's kernels and the 8-bit
+// activation checkpoints: the activation functions, and the 8-bit codec.
+#pragma once
+
+#include <float.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace qnf4 {
+
+// ---------------------------------------------------------------------------
+// act(g) = g * s with s = 1 / (1 + exp(-z)):
+//   silu         z = g                               act' = s + g s (1 - s)
+//   gelu (tanh)  z = 2 sqrt(2/pi) (g + 0.044715 g^3)  act' = s + g s (1 - s) z'
+// (0.5 (1 + tanh(y)) = 1 / (1 + exp(-2 y)), which keeps its relative precision
+// where the sum 1 + tanh cancels).  The exponential is the hardware's base-2
+// one: a relative error below 2^-21 over the range that matters, against the
+// 2^-9 of the bf16 result.
+// ---------------------------------------------------------------------------
+constexpr float kGelu2K = 1.5957691216057308f;    // 2 sqrt(2/pi)
+constexpr float kGelu2KC = 0.07135481282679626f;  // 2 sqrt(2/pi) * 0.044715
+constexpr float kLog2E = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / (1 + exp(-z))
+__device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + ex2(-z * kLog2E)); }
+
+__device__ __forceinline__ float act_value(int act, float g) {
+  const float z = act == QLORA_ACT_SILU ? g : g * fmaf(kGelu2KC * g, g, kGelu2K);
+  return g * logistic(z);
+}
+
+// act(g), and its derivative in `d`
+__device__ __forceinline__ float act_value_grad(int act, float g, float& d) {
+  const float g2 = g * g;
+  const bool silu = act == QLORA_ACT_SILU;
+  const float z = silu ? g : g * fmaf(kGelu2KC, g2, kGelu2K);
+  const float dz = silu ? 1.0f : fmaf(3.0f * kGelu2KC, g2, kGelu2K);
+  const float s = logistic(z);
+  const float a = g * s;
+  // 1 - s = 1 / (1 + exp(z)): where it has underflowed a * 0 must stay 0
+  // although dz may have overflowed
+  const float t = a * (1.0f - s);
+  d = t == 0.0f ? s : fmaf(t, dz, s);
+  return a;
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit activation checkpoint: a row is cut into blocks of 64; scale
+// s = fl32(amax / 127), or 1 where that is below the normal fp32 range (an
+// all-zero block among them); code q = rint(fl32(x / s)), ties to even;
+// value = bf16(fl32(q * s)).
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float act8_scale(float amax) {
+  const float s = __fdiv_rn(amax, 127.0f);
+  return s >= FLT_MIN ? s : 1.0f;
+}
+
+// rint(fl32(x / s)).  x * inv is within 127 * 2^-22 of x / s (two roundings of
+// a magnitude of at most 127), so the two round alike unless the product is
+// within 2^-14 of a tie; only then is the division carried out.
+__device__ __forceinline__ int act8_code(float x, float s, float inv) {
+  const float t = x * inv;
+  float q = rintf(t);
+  if (fabsf(fabsf(t - q) - 0.5f) < 6.103515625e-05f) q = rintf(__fdiv_rn(x, s));
+  return static_cast<int>(q);
+}
+
+// The code's value before its rounding to bf16.
+__device__ __forceinline__ float act8_value(int8_t q, float s) { return static_cast<float>(q) * s; }
+
+}  // namespace qnf4

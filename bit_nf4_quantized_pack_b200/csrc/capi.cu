@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <cmath>
+#include <initializer_list>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -321,6 +322,241 @@ qlora_status qlora_linear_bwd(int64_t M, int64_t K, int64_t N, int32_t r, const 
                                           dX, dA, dB, ws, ws_bytes, d_status,
                                           reinterpret_cast<cudaStream_t>(stream), sms);
   return cuda_status(e);
+}
+
+namespace {
+
+// An 8-bit checkpoint of rows x cols (any shape when rows < 0).
+qlora_status check_act8(const qlora_act8* a, int64_t rows, int64_t cols) {
+  if (!a || !a->codes || !a->scales || !aligned(a->codes, 16) || !aligned(a->scales, 16))
+    return QLORA_ERR_INVALID_ARG;
+  if (a->rows < 1 || a->cols < 1) return QLORA_ERR_INVALID_ARG;
+  if (rows >= 0 && (a->rows != rows || a->cols != cols)) return QLORA_ERR_INVALID_ARG;
+  if (a->cols % 64 != 0) return QLORA_ERR_UNSUPPORTED;
+  if (a->cols > kMaxNumel || a->rows > kMaxNumel / a->cols) return QLORA_ERR_UNSUPPORTED;
+  return QLORA_OK;
+}
+
+bool grad_type(qlora_dtype t) { return t == QLORA_DTYPE_BF16 || t == QLORA_DTYPE_F32; }
+
+bool all_aligned16(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (!p || !aligned(p, 16)) return false;
+  return true;
+}
+
+// Sizes, weights, adapters and scalars of the gated block.
+qlora_status check_gated(int64_t M, int64_t K, int64_t N, int32_t r, const qlora_nf4_state* Wg,
+                         const qlora_nf4_state* Wu, const uint16_t* Ag, const uint16_t* Bg,
+                         const uint16_t* Au, const uint16_t* Bu, float c, qlora_act act) {
+  qlora_status v = check_linear_shape(M, K, N, r);
+  if (v != QLORA_OK) return v;
+  if (M > kMaxNumel / N || M > kMaxNumel / K) return QLORA_ERR_UNSUPPORTED;
+  for (const qlora_nf4_state* W : {Wg, Wu}) {
+    v = check_state(W, true);
+    if (v != QLORA_OK) return v;
+    if (W->numel != K * N) return QLORA_ERR_INVALID_ARG;
+  }
+  if (!std::isfinite(c)) return QLORA_ERR_INVALID_ARG;
+  if (act != QLORA_ACT_SILU && act != QLORA_ACT_GELU) return QLORA_ERR_INVALID_ARG;
+  return all_aligned16({Ag, Bg, Au, Bu}) ? QLORA_OK : QLORA_ERR_INVALID_ARG;
+}
+
+// The kept buffers: Zg, Zu and g, u in exactly one of the two forms.
+qlora_status check_saved(const qlora_gated_saved* s, qnf4::GatedKept* k) {
+  if (!all_aligned16({s->Zg, s->Zu})) return QLORA_ERR_INVALID_ARG;
+  const bool wide = s->G || s->U, narrow = s->G8 || s->U8 || s->G_scales || s->U_scales;
+  if (wide == narrow) return QLORA_ERR_INVALID_ARG;
+  if (wide && !all_aligned16({s->G, s->U})) return QLORA_ERR_INVALID_ARG;
+  if (narrow && !all_aligned16({s->G8, s->U8, s->G_scales, s->U_scales})) return QLORA_ERR_INVALID_ARG;
+  *k = qnf4::GatedKept{s->G, s->U, s->G8, s->U8, s->G_scales, s->U_scales, s->Zg, s->Zu};
+  return QLORA_OK;
+}
+
+qnf4::GatedWeights gated_weights(const qlora_nf4_state* Wg, const qlora_nf4_state* Wu, const uint16_t* Ag,
+                                 const uint16_t* Bg, const uint16_t* Au, const uint16_t* Bu, float c,
+                                 qlora_act act) {
+  return qnf4::GatedWeights{Wg->packed, Wu->packed, view_of(Wg), view_of(Wu), Ag, Bg, Au, Bu, c, act};
+}
+
+qlora_status check_head(int64_t M, int64_t K, int64_t N) {
+  const qlora_status v = check_linear_shape(M, K, N, 1);
+  if (v != QLORA_OK) return v;
+  return M > kMaxNumel / N || M > kMaxNumel / K ? QLORA_ERR_UNSUPPORTED : QLORA_OK;
+}
+
+}  // namespace
+
+qlora_status qlora_act8_quantize(const uint16_t* X, const qlora_act8* out, int32_t* d_status,
+                                 qlora_stream_t stream) {
+  NvtxRange nvtx_range("qlora_act8_quantize");
+  const qlora_status v = check_act8(out, -1, -1);
+  if (v != QLORA_OK) return v;
+  if (!X || !aligned(X, 16)) return QLORA_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  if (sms <= 0) return QLORA_ERR_CUDA;
+  return cuda_status(qnf4::launch_act8_quantize(X, out->rows * out->cols, out->codes, out->scales, d_status,
+                                                reinterpret_cast<cudaStream_t>(stream), sms));
+}
+
+qlora_status qlora_act8_dequantize(const qlora_act8* in, uint16_t* X, qlora_stream_t stream) {
+  NvtxRange nvtx_range("qlora_act8_dequantize");
+  const qlora_status v = check_act8(in, -1, -1);
+  if (v != QLORA_OK) return v;
+  if (!X || !aligned(X, 16)) return QLORA_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  if (sms <= 0) return QLORA_ERR_CUDA;
+  return cuda_status(qnf4::launch_act8_dequantize(in->codes, in->scales, in->rows * in->cols, X,
+                                                  reinterpret_cast<cudaStream_t>(stream), sms));
+}
+
+qlora_status qlora_linear_bwd_act8(int64_t M, int64_t K, int64_t N, int32_t r, const uint16_t* dY,
+                                   const uint16_t* X, const qlora_act8* X8, const uint16_t* Zc,
+                                   const qlora_nf4_state* W, const uint16_t* A, const uint16_t* B,
+                                   float c, uint16_t* dX, void* dA, void* dB, qlora_dtype grad_dtype,
+                                   void* ws, size_t ws_bytes, int32_t* d_status,
+                                   qlora_stream_t stream) {
+  NvtxRange nvtx_range("qlora_linear_bwd_act8");
+  qlora_status v = check_linear_shape(M, K, N, r);
+  if (v != QLORA_OK) return v;
+  if (M > kMaxNumel / N || M > kMaxNumel / K) return QLORA_ERR_UNSUPPORTED;
+  v = check_state(W, true);
+  if (v != QLORA_OK) return v;
+  if (W->numel != K * N || !std::isfinite(c) || !grad_type(grad_dtype)) return QLORA_ERR_INVALID_ARG;
+  if ((X != nullptr) == (X8 != nullptr)) return QLORA_ERR_INVALID_ARG;
+  if (X8) {
+    v = check_act8(X8, M, K);
+    if (v != QLORA_OK) return v;
+    if (!Zc) return QLORA_ERR_INVALID_ARG;
+  } else if (!aligned(X, 16)) {
+    return QLORA_ERR_INVALID_ARG;
+  }
+  if (!all_aligned16({dY, A, B, dX, dA, dB}) || (Zc && !aligned(Zc, 16))) return QLORA_ERR_INVALID_ARG;
+  const size_t need = qlora_linear_bwd_workspace_size(M, K, N, r);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned(ws, 16))) return QLORA_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  if (sms <= 0) return QLORA_ERR_CUDA;
+  return cuda_status(qnf4::launch_linear_bwd(
+      M, K, N, r, dY, X, Zc, W->packed, view_of(W), A, B, c, dX, dA, dB, ws, ws_bytes, d_status,
+      reinterpret_cast<cudaStream_t>(stream), sms, grad_dtype == QLORA_DTYPE_BF16,
+      X8 ? X8->codes : nullptr, X8 ? X8->scales : nullptr));
+}
+
+size_t qlora_gated_fwd_workspace_size(int64_t M, int64_t K, int64_t N, int32_t r) {
+  if (check_linear_shape(M, K, N, r) != QLORA_OK || M > kMaxNumel / N || M > kMaxNumel / K) return 0;
+  return qnf4::gated_fwd_workspace_bytes(M, K, N, r);
+}
+
+size_t qlora_gated_bwd_workspace_size(int64_t M, int64_t K, int64_t N, int32_t r) {
+  if (check_linear_shape(M, K, N, r) != QLORA_OK || M > kMaxNumel / N || M > kMaxNumel / K) return 0;
+  return qnf4::gated_bwd_workspace_bytes(M, K, N, r);
+}
+
+qlora_status qlora_gated_fwd(int64_t M, int64_t K, int64_t N, int32_t r, const uint16_t* X,
+                             const qlora_nf4_state* Wg, const qlora_nf4_state* Wu,
+                             const uint16_t* Ag, const uint16_t* Bg, const uint16_t* Au,
+                             const uint16_t* Bu, float c, qlora_act act, uint16_t* H,
+                             const qlora_gated_saved* saved, void* ws, size_t ws_bytes,
+                             int32_t* d_status, qlora_stream_t stream) {
+  NvtxRange nvtx_range("qlora_gated_fwd");
+  qlora_status v = check_gated(M, K, N, r, Wg, Wu, Ag, Bg, Au, Bu, c, act);
+  if (v != QLORA_OK) return v;
+  if (!all_aligned16({X, H})) return QLORA_ERR_INVALID_ARG;
+  qnf4::GatedKept kept{};
+  if (saved) {
+    v = check_saved(saved, &kept);
+    if (v != QLORA_OK) return v;
+  }
+  const size_t need = qlora_gated_fwd_workspace_size(M, K, N, r);
+  if (!ws || ws_bytes < need || !aligned(ws, 16)) return QLORA_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  if (sms <= 0) return QLORA_ERR_CUDA;
+  return cuda_status(qnf4::launch_gated_fwd(M, K, N, r, X, gated_weights(Wg, Wu, Ag, Bg, Au, Bu, c, act), H,
+                                            kept, ws, ws_bytes, d_status,
+                                            reinterpret_cast<cudaStream_t>(stream), sms));
+}
+
+qlora_status qlora_gated_bwd(int64_t M, int64_t K, int64_t N, int32_t r, const uint16_t* dH,
+                             const uint16_t* X, const qlora_act8* X8,
+                             const qlora_gated_saved* saved, const qlora_nf4_state* Wg,
+                             const qlora_nf4_state* Wu, const uint16_t* Ag, const uint16_t* Bg,
+                             const uint16_t* Au, const uint16_t* Bu, float c, qlora_act act,
+                             uint16_t* dX, void* dAg, void* dBg, void* dAu, void* dBu,
+                             qlora_dtype grad_dtype, void* ws, size_t ws_bytes, int32_t* d_status,
+                             qlora_stream_t stream) {
+  NvtxRange nvtx_range("qlora_gated_bwd");
+  qlora_status v = check_gated(M, K, N, r, Wg, Wu, Ag, Bg, Au, Bu, c, act);
+  if (v != QLORA_OK) return v;
+  if (!grad_type(grad_dtype) || !saved || (X != nullptr) == (X8 != nullptr)) return QLORA_ERR_INVALID_ARG;
+  qnf4::GatedKept kept{};
+  v = check_saved(saved, &kept);
+  if (v != QLORA_OK) return v;
+  if (X8) {
+    v = check_act8(X8, M, K);
+    if (v != QLORA_OK) return v;
+  } else if (!aligned(X, 16)) {
+    return QLORA_ERR_INVALID_ARG;
+  }
+  if (!all_aligned16({dH, dX, dAg, dBg, dAu, dBu})) return QLORA_ERR_INVALID_ARG;
+  const size_t need = qlora_gated_bwd_workspace_size(M, K, N, r);
+  if (!ws || ws_bytes < need || !aligned(ws, 16)) return QLORA_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  if (sms <= 0) return QLORA_ERR_CUDA;
+  return cuda_status(qnf4::launch_gated_bwd(
+      M, K, N, r, dH, X, X8 ? X8->codes : nullptr, X8 ? X8->scales : nullptr,
+      gated_weights(Wg, Wu, Ag, Bg, Au, Bu, c, act), kept, dX, dAg, dBg, dAu, dBu,
+      grad_dtype == QLORA_DTYPE_BF16, ws, ws_bytes, d_status, reinterpret_cast<cudaStream_t>(stream), sms));
+}
+
+size_t qlora_head_loss_fwd_workspace_size(int64_t M, int64_t K, int64_t N) {
+  return check_head(M, K, N) == QLORA_OK ? qnf4::loss_fwd_workspace_bytes(M, N) : 0;
+}
+
+size_t qlora_head_loss_bwd_workspace_size(int64_t M, int64_t K, int64_t N) {
+  return check_head(M, K, N) == QLORA_OK ? qnf4::loss_bwd_workspace_bytes(M, K, N) : 0;
+}
+
+qlora_status qlora_head_loss_fwd(int64_t M, int64_t K, int64_t N, int64_t vocab, const uint16_t* X,
+                                 const qlora_nf4_state* W, const int64_t* labels,
+                                 int64_t ignore_index, float* loss, float* lse, void* ws,
+                                 size_t ws_bytes, int32_t* d_status, qlora_stream_t stream) {
+  NvtxRange nvtx_range("qlora_head_loss_fwd");
+  qlora_status v = check_head(M, K, N);
+  if (v != QLORA_OK) return v;
+  v = check_state(W, true);
+  if (v != QLORA_OK) return v;
+  if (W->numel != K * N || vocab < 1 || vocab > N) return QLORA_ERR_INVALID_ARG;
+  if (!X || !aligned(X, 16) || !labels || !aligned(labels, 8)) return QLORA_ERR_INVALID_ARG;
+  if (!loss || !aligned(loss, 4) || !lse || !aligned(lse, 4)) return QLORA_ERR_INVALID_ARG;
+  const size_t need = qlora_head_loss_fwd_workspace_size(M, K, N);
+  if (!ws || ws_bytes < need || !aligned(ws, 16)) return QLORA_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  if (sms <= 0) return QLORA_ERR_CUDA;
+  return cuda_status(qnf4::launch_loss_fwd(M, K, N, vocab, X, W->packed, view_of(W), labels, ignore_index,
+                                           loss, lse, ws, ws_bytes, d_status,
+                                           reinterpret_cast<cudaStream_t>(stream), sms));
+}
+
+qlora_status qlora_head_loss_bwd(int64_t M, int64_t K, int64_t N, int64_t vocab,
+                                 const float* dloss, const uint16_t* X, const float* lse,
+                                 const qlora_nf4_state* W, const int64_t* labels,
+                                 int64_t ignore_index, uint16_t* dX, void* ws, size_t ws_bytes,
+                                 int32_t* d_status, qlora_stream_t stream) {
+  NvtxRange nvtx_range("qlora_head_loss_bwd");
+  qlora_status v = check_head(M, K, N);
+  if (v != QLORA_OK) return v;
+  v = check_state(W, true);
+  if (v != QLORA_OK) return v;
+  if (W->numel != K * N || vocab < 1 || vocab > N) return QLORA_ERR_INVALID_ARG;
+  if (!all_aligned16({X, dX}) || !labels || !aligned(labels, 8)) return QLORA_ERR_INVALID_ARG;
+  if (!dloss || !aligned(dloss, 4) || !lse || !aligned(lse, 4)) return QLORA_ERR_INVALID_ARG;
+  const size_t need = qlora_head_loss_bwd_workspace_size(M, K, N);
+  if (!ws || ws_bytes < need || !aligned(ws, 16)) return QLORA_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  if (sms <= 0) return QLORA_ERR_CUDA;
+  return cuda_status(qnf4::launch_loss_bwd(M, K, N, vocab, dloss, X, lse, W->packed, view_of(W), labels,
+                                           ignore_index, dX, ws, ws_bytes, d_status,
+                                           reinterpret_cast<cudaStream_t>(stream), sms));
 }
 
 }  // extern "C"

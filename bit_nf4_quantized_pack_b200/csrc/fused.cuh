@@ -1,0 +1,920 @@
+// The fused NF4-decode GEMM on sm_100a, shared by the layer (linear.cu) and the
+// operators built on it (gated.cu, loss.cu).  Every translation unit that
+// includes this file gets its own copy of what it uses.
+#pragma once
+
+#include <math_constants.h>
+
+#include "act.cuh"
+#include "common.cuh"
+#include "kernels.cuh"
+#include "profile.cuh"
+#include "tmap.cuh"
+
+namespace qnf4 {
+namespace {
+
+// code values of the two codebooks: [0, 16) NF4, [16, 32) uniform INT4
+__constant__ float kNF4g[32] = {QNF4_TABLE_VALUES, QNF4_INT4_VALUES};
+
+// ===========================================================================
+// Fused NF4-decode GEMM.  kMode:
+//   kModeFwd        Y = X·Ŵ + Zc·B
+//   kModeBwd        dX = G·Ŵᵀ + dZ·Aᵀ
+//   kModeGatedFwd   g = X·Ŵg + Zg·Bg and u = X·Ŵu + Zu·Bu side by side, H = act(g)·u
+//   kModeGatedBwd   dX = dG·Ŵgᵀ + dU·Ŵuᵀ + dZg·Agᵀ + dZu·Auᵀ
+//   kModeLossStats  the maximum and sum of exponentials of each row of X·Ŵ over
+//                   256 columns, and the label's logit
+//   kModeLossGrad   bf16 of dloss·(softmax(X·Ŵ) - onehot) over a piece of columns
+//   kModeLossDX     dX (+)= P·Ŵᵀ over a piece of columns
+// "forward" and "backward" below are the operand layouts: the modes with Ŵᵀ
+// (Bwd, GatedBwd, LossDX) use the backward one.
+//
+// Persistent pairs of CTAs on neighbouring SMs (a 1 x 2 thread-block cluster)
+// run CTA-pair tensor-core products (tcgen05.mma.cta_group::2, M = 256,
+// N = 256, K = 16), issued by CTA rank 0 for both: the A operand is split by
+// rows (128 per CTA) and the B operand by columns (128 per CTA), each half in
+// its own CTA's shared memory, and each CTA's TMEM receives its 128 rows of D
+// over all 256 columns.  So each CTA stages only half of each operand, and
+// the tensor core reads 8 KB of shared memory per CTA and 16-wide K slice
+// for a 128 x 256 x 16 product per SM.
+//   forward   pair tile 512 rows x 256 columns; CTA q holds rows
+//             m0 + 256q + [0, 256) (slices h = 0, 1 of 128 rows, the K-major
+//             A operand of accumulator h) and decodes columns n0 + 128q + [0,
+//             128) of every weight K-step (the MN-major B operand);
+//   backward  transposed: pair tile 256 output columns x 512 dY rows; CTA q
+//             decodes the weight rows n0 + 128q + [0, 128) (the K-major A
+//             operand: its output columns) and holds dY rows m0 + 256h + 128q +
+//             [0, 128) (its half of the B operand of accumulator h = 0, 1).
+// TMEM: two accumulators of 128 lanes x 256 fp32 columns per CTA (all 512).
+//
+// Shared memory holds two rings per CTA.  Activation tiles (256 x 64 bf16,
+// K-major, two TMA boxes of 128 rows) have 4 stages; TMA loads of both CTAs
+// complete on CTA 0's barrier (the cta_group::2 form of the copy), which CTA
+// 0's producer arms with both CTAs' bytes.  Decoded weight tiles have 4
+// stages; decoder warps write them as 128 rows of 128 bytes, each row one NF4
+// block of 64 consecutive weights (row R at R*128, 16-byte chunk c at
+// (c ^ (R & 7))*16, the 128-byte swizzle pattern):
+//   forward   row R = 64*nb + k: weights (k0+k, n0+128q+64nb .. +63) — an
+//             MN-major operand (atoms of 8 k-rows x 64 n; 8 KB between
+//             n-atoms);
+//   backward  row R: weights (n0+128q+R, k0 .. k0+63) of W, i.e. row R of
+//             Ŵᵀ's K-major operand.
+// Each decoder thread owns one row and loads its 32 packed bytes and its
+// block scale straight from global memory K-steps ahead; both CTAs' decoder
+// warps arrive on CTA 0's barrier of the stage.  The MMA's commit releases
+// the stages and signals the accumulators in both CTAs (multicast), and both
+// CTAs' epilogue warps release an accumulator on CTA 0's barrier.
+//
+// After the last K-step of a tile, the LoRA step takes two activation stages:
+// Zc (or dZ) as the activation tile and B (or A) as the weight tile, both by
+// TMA with the rank padded to a multiple of 16 by TMA's zero fill; the decoder
+// warps skip it.  The epilogue releases each accumulator as soon as it has
+// read it, so the next tile's first MMAs overlap the drain of the last.  In
+// the backward a warp's TMEM load gives each lane one output column over 32
+// consecutive rows, so every store instruction writes 32 adjacent bf16 of one
+// output row.
+//
+// The gated forward is the forward with another meaning of the 256 columns of
+// a pair tile: CTA 0 decodes 128 columns of the gate weight, CTA 1 the same
+// 128 columns of the up weight, so a row's g and u meet in one thread of the
+// epilogue and the decode per product stays that of one weight.  Its two LoRA
+// steps give each CTA the rows of its own B and zeros (a box past the
+// matrix's last row) in the other's step.  The gated backward runs through
+// the K-steps of dG·Ŵgᵀ and then of dU·Ŵuᵀ in the same accumulators.
+// These modes and the loss's split activation rows as m0 + 256h + 128q and
+// leave out slice h = 1 where a tile has no more than 256 rows.
+// ===========================================================================
+enum FusedMode : int {
+  kModeFwd = 0,
+  kModeBwd = 1,
+  kModeGatedFwd = 2,
+  kModeGatedBwd = 3,
+  kModeLossStats = 4,
+  kModeLossGrad = 5,
+  kModeLossDX = 6
+};
+constexpr bool mode_transposed(int m) { return m == kModeBwd || m == kModeGatedBwd || m == kModeLossDX; }
+constexpr bool mode_gated(int m) { return m == kModeGatedFwd || m == kModeGatedBwd; }
+constexpr bool mode_loss(int m) { return m >= kModeLossStats; }
+constexpr int mode_lora_steps(int m) { return mode_loss(m) ? 0 : (mode_gated(m) ? 2 : 1); }
+constexpr int mode_tile_cols(int m) { return m == kModeGatedFwd ? 128 : 256; }
+
+constexpr int kFAStages = 4;          // activation tiles (TMA)
+constexpr int kFBStages = 4;          // decoded weight tiles (decoder warps)
+constexpr int kFBN = 128;             // decoded rows per CTA and K-step
+constexpr int kFSlices = 2;           // 128-row activation slices per CTA = accumulators
+constexpr int kFAccCols = 256;        // TMEM columns per accumulator (the pair MMA's N)
+constexpr int kFPairRows = 512;       // activation rows of a pair tile
+constexpr int kFPairCols = 256;       // output columns of a pair tile
+constexpr int kFA = kFSlices * 128 * 128;   // 256 x 64 bf16
+constexpr int kFB = kFBN * 128;             // 128 x 64 bf16
+constexpr int kFDecWarps = kFBN / 32;       // one weight-tile row per decoder thread and K-step
+// Decoder groups of kFDecWarps warps take turns by K-step (group g decodes the
+// steps g, g + kFDecGroups, ...), so each warp has kFDecGroups K-steps of time
+// per row and its loads reach further ahead.
+constexpr int kFDecGroups = 2;
+constexpr int kFDecAll = kFDecWarps * kFDecGroups;
+constexpr int kFEpiWarps = 4;
+constexpr int kFThreads = (2 + kFDecAll + kFEpiWarps) * 32;  // TMA, MMA, decoders, epilogue
+constexpr size_t kFSmem = 1024 + kFAStages * kFA + kFBStages * kFB + 1024 + 512;
+static_assert(kFSlices * kFAccCols == 512 && kFBN == 128, "accumulators fill TMEM");
+static_assert(kFSmem <= 232448, "fused kernel shared memory");
+
+struct FusedArgs {
+  int M;          // rows of the activation / output
+  int Nout;       // output columns (forward: N, backward: K; loss: columns of the piece)
+  int Nw;         // row length of the weight (N); blocks per weight row = Nw/64
+  int nk;         // K-steps over the contraction (forward: K/64, backward: N/64)
+  int rsteps;     // MMAs of K=16 in a LoRA step (ceil(r/16))
+  int m_tiles, n_tiles;
+  ScaleView sv;
+  const uint8_t* packed;
+  uint16_t* out;  // bf16 [M][Nout]
+  int32_t* d_status;
+};
+
+// What the gated modes need besides: the second weight (nk counts the K-steps
+// of both in the backward), and in the forward the activation and the buffers
+// that keep g and u for the backward (all null: nothing is kept).
+struct GatedArgs : FusedArgs {
+  ScaleView sv2;
+  const uint8_t* packed2;
+  int act;
+  uint16_t *G, *U;      // bf16 [M][Nout], or
+  int8_t *G8, *U8;      // 8-bit codes [M][Nout] with scales [M][Nout/64]
+  float *Gs, *Us;
+};
+
+// What the loss modes need besides.  The weight's columns col0 .. col0 + Nout
+// are the piece; columns from `vocab` on do not exist for the softmax.
+struct LossArgs : FusedArgs {
+  int col0;
+  int vocab;
+  const int64_t* labels;
+  int64_t ignore_index;
+  const float* lse;     // LossGrad
+  const float* dloss;   // LossGrad
+  float2* stats;        // LossStats: [n_tiles][M] (maximum, sum of exponentials)
+  float* label_logit;   // LossStats: [M]
+  float* acc;           // LossDX: fp32 [M][Nout] sums over the pieces
+  int first, last;      // LossDX: no piece before / after this one
+};
+
+template <int kMode>
+struct ModeTypes {
+  struct Maps { CUtensorMap act, la, lb; };
+  using Args = FusedArgs;
+};
+struct MapsPair { CUtensorMap act, la, lb, act2, la2, lb2; };
+struct MapsOne { CUtensorMap act; };
+template <> struct ModeTypes<kModeGatedFwd> { using Maps = MapsPair; using Args = GatedArgs; };
+template <> struct ModeTypes<kModeGatedBwd> { using Maps = MapsPair; using Args = GatedArgs; };
+template <> struct ModeTypes<kModeLossStats> { using Maps = MapsOne; using Args = LossArgs; };
+template <> struct ModeTypes<kModeLossGrad> { using Maps = MapsOne; using Args = LossArgs; };
+template <> struct ModeTypes<kModeLossDX> { using Maps = MapsOne; using Args = LossArgs; };
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+
+// 8 packed nibbles (4 bytes, first weight in the high nibble of byte 0) ->
+// 8 bf16 from the per-block table whose high and low bytes are split into
+// H[0..3] and L[0..3] (entry j's byte in byte j%4 of H[j/4] / L[j/4]).
+__device__ __forceinline__ uint4 decode8(uint32_t p, const uint32_t (&H)[4],
+                                         const uint32_t (&L)[4]) {
+  // selector nibbles: low 3 bits pick a byte within a plane pair, bit 3
+  // (moved to the "+4" position) picks the pair
+  const uint32_t s = p & 0x77777777u;
+  const uint32_t b = ((p >> 1) & 0x44444444u) | 0x32103210u;
+  uint4 o;
+  {
+    const uint32_t hF = prmt(prmt(H[0], H[1], s), prmt(H[2], H[3], s), b);
+    const uint32_t lF = prmt(prmt(L[0], L[1], s), prmt(L[2], L[3], s), b);
+    o.x = prmt(lF, hF, 0x4051u);
+    o.y = prmt(lF, hF, 0x6273u);
+  }
+  {
+    const uint32_t s2 = s >> 16, b2 = b >> 16;
+    const uint32_t hF = prmt(prmt(H[0], H[1], s2), prmt(H[2], H[3], s2), b2);
+    const uint32_t lF = prmt(prmt(L[0], L[1], s2), prmt(L[2], L[3], s2), b2);
+    o.z = prmt(lF, hF, 0x4051u);
+    o.w = prmt(lF, hF, 0x6273u);
+  }
+  return o;
+}
+
+// Per-block table: entry j = bf16(C_j * a) (fp32 product, then bf16).
+__device__ __forceinline__ void build_lut(const float* C, float a, uint32_t (&H)[4], uint32_t (&L)[4]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(C[2 * i] * a, C[2 * i + 1] * a);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    H[q] = prmt(w[2 * q], w[2 * q + 1], 0x7531u);
+    L[q] = prmt(w[2 * q], w[2 * q + 1], 0x6420u);
+  }
+}
+
+// What one decoder thread needs for one K-step, loaded ahead of use.
+struct RowFetch {
+  uint4 p0, p1;   // 32 packed bytes of the row's NF4 block
+  float absv;     // absmax (no double quant)
+  uint32_t q;     // scale code (double quant)
+  float s2v;      // second-level scale (double quant)
+  bool valid;     // row inside the weight; false also for LoRA steps
+  bool second;    // the gated backward's second weight
+};
+
+// Row R of the decoded tile of CTA `rank` at K-step kk.
+template <int kMode>
+__device__ __forceinline__ RowFetch fetch_row(const typename ModeTypes<kMode>::Args& a, int tile, int kk,
+                                              int R, int rank, int num_tiles) {
+  RowFetch f;
+  f.p0 = make_uint4(0, 0, 0, 0);
+  f.p1 = f.p0;
+  f.absv = 1.0f;
+  f.q = 0;
+  f.s2v = 1.0f;
+  f.valid = false;
+  f.second = false;
+  if (tile >= num_tiles || kk >= a.nk) return f;
+  const int n0 = (tile / a.m_tiles) * mode_tile_cols(kMode);
+  const int64_t rowbytes = a.Nw / 2;
+  const int64_t bpr = a.Nw / 64;
+  const uint8_t* packed = a.packed;
+  const ScaleView* sv = &a.sv;
+  if constexpr (kMode == kModeGatedFwd) {
+    if (rank != 0) { packed = a.packed2; sv = &a.sv2; }
+  }
+  if constexpr (kMode == kModeGatedBwd) {
+    if (kk >= a.nk / 2) {
+      f.second = true;
+      kk -= a.nk / 2;
+      packed = a.packed2;
+      sv = &a.sv2;
+    }
+  }
+  int64_t blk;
+  const uint8_t* src;
+  if constexpr (!mode_transposed(kMode)) {
+    // columns of the tile: 128 per CTA, or the same 128 of each weight
+    const int Rg = kMode == kModeGatedFwd ? R : kFBN * rank + R;
+    const int nb = Rg >> 6, kr = Rg & 63;
+    if (n0 + nb * 64 >= a.Nout) return f;
+    int col = n0 + nb * 64;
+    if constexpr (mode_loss(kMode)) col += a.col0;
+    const int64_t k = static_cast<int64_t>(kk) * 64 + kr;
+    src = packed + k * rowbytes + col / 2;
+    blk = k * bpr + col / 64;
+  } else {
+    const int Rg = kFBN * rank + R;
+    if (n0 + Rg >= a.Nout) return f;
+    const int64_t kw = n0 + Rg;
+    int cb = kk;
+    if constexpr (mode_loss(kMode)) cb += a.col0 / 64;
+    src = packed + kw * rowbytes + static_cast<int64_t>(cb) * 32;
+    blk = kw * bpr + cb;
+  }
+  f.valid = true;
+  // volatile asm: the loads issue here, K-steps before their use, instead of
+  // being moved down to it
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(f.p0.x), "=r"(f.p0.y), "=r"(f.p0.z), "=r"(f.p0.w) : "l"(src));
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(f.p1.x), "=r"(f.p1.y), "=r"(f.p1.z), "=r"(f.p1.w) : "l"(src + 16));
+  if (sv->code8 == nullptr) {
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(f.absv) : "l"(sv->absmax + blk));
+  } else {
+    uint16_t qv;
+    asm volatile("ld.global.nc.u8 %0, [%1];" : "=h"(qv) : "l"(sv->code8 + blk));
+    f.q = qv;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(f.s2v) : "l"(sv->s2 + (blk >> 8)));
+  }
+  return f;
+}
+
+// Advance an iteration cursor (tile, kk) by `n` steps of nsteps per tile;
+// consecutive tiles of one pair are `stride` apart.
+__device__ __forceinline__ void advance(int& tile, int& kk, int n, int nsteps, int stride) {
+  kk += n;
+  while (kk >= nsteps) {
+    kk -= nsteps;
+    tile += stride;
+  }
+}
+
+// Slices of 128 rows per CTA of the tile that starts at row m0 which hold rows
+// of the activation (the layer's own modes always run both).
+template <int kMode>
+__device__ __forceinline__ int tile_slices(int M, int m0) {
+  if (kMode == kModeFwd || kMode == kModeBwd) return kFSlices;
+  return M - m0 > 256 ? 2 : 1;
+}
+
+// 32 fp32 values as 32 bf16 (64 bytes, 16-byte aligned)
+__device__ __forceinline__ void store_bf16x32(uint16_t* dst, const float (&v)[32]) {
+  uint4* d = reinterpret_cast<uint4*>(dst);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    d[i] = make_uint4(pack_bf16x2(v[8 * i + 0], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                      pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+}
+
+__device__ __forceinline__ float round_bf16(float x) {
+  return __uint_as_float(pack_bf16x2(x, 0.0f) << 16);
+}
+
+// The 8-bit codes of 64 accumulator columns rounded to bf16, exactly as
+// qlora_act8_quantize would form them from the bf16 matrix: one pass over the
+// columns for their largest magnitude, one for the codes (TMEM is read again
+// rather than 64 values held).
+__device__ __forceinline__ void store_act8_block(uint32_t taddr, bool in, int8_t* codes, float* scale,
+                                                 int32_t* d_status) {
+  float amax = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t v[32];
+    __syncwarp();
+    tmem_ld_32x32b_x32(taddr + c * 32, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) amax = fmax_nan(amax, fabsf(round_bf16(__uint_as_float(v[i]))));
+  }
+  const float s = act8_scale(amax);
+  const float inv = __frcp_rn(s);
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t v[32];
+    __syncwarp();
+    tmem_ld_32x32b_x32(taddr + c * 32, v);
+    tmem_ld_wait();
+    if (in) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[i] |= (static_cast<uint32_t>(act8_code(round_bf16(__uint_as_float(v[4 * i + j])), s, inv)) & 0xFFu)
+                  << (8 * j);
+      }
+      uint4* d = reinterpret_cast<uint4*>(codes + c * 32);
+      d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+  if (in) {
+    *scale = s;
+    if (!(amax <= FLT_MAX)) raise_status(d_status, QLORA_ERR_NONFINITE);
+  }
+}
+
+// Gated forward: this lane's row of 128 g (columns 0 .. 127 of the
+// accumulator) and 128 u (128 .. 255).  All lanes run every TMEM load; rows
+// past M store nothing.
+__device__ __forceinline__ void epilogue_gated(const GatedArgs& a, uint32_t tbase, int row, int n0) {
+  const bool in = row < a.M;
+  const int64_t base = static_cast<int64_t>(row) * a.Nout + n0;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    if (n0 + c * 32 >= a.Nout) break;   // the same for the whole warp
+    __syncwarp();                       // the TMEM load takes the whole warp
+    uint32_t vg[32], vu[32];
+    tmem_ld_32x32b_x32(tbase + c * 32, vg);
+    tmem_ld_32x32b_x32(tbase + 128 + c * 32, vu);
+    tmem_ld_wait();
+    if (in) {
+      float h[32];
+      if (a.G != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) h[i] = __uint_as_float(vg[i]);
+        store_bf16x32(a.G + base + c * 32, h);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) h[i] = __uint_as_float(vu[i]);
+        store_bf16x32(a.U + base + c * 32, h);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) h[i] = act_value(a.act, __uint_as_float(vg[i])) * __uint_as_float(vu[i]);
+      store_bf16x32(a.out + base + c * 32, h);
+    }
+  }
+  if (a.G8 != nullptr) {
+    const int64_t bpr = a.Nout / 64;
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+      const int col = n0 + (b & 1) * 64;
+      if (col >= a.Nout) continue;      // the same for the whole warp
+      int8_t* codes = b < 2 ? a.G8 : a.U8;
+      float* scales = b < 2 ? a.Gs : a.Us;
+      store_act8_block(tbase + b * 64, in, codes + static_cast<int64_t>(row) * a.Nout + col,
+                       scales + static_cast<int64_t>(row) * bpr + col / 64, a.d_status);
+    }
+  }
+}
+
+// Loss statistics of this lane's row over the tile's 256 columns: the running
+// maximum m and the sum s of exp(l - m), and the label's logit where the
+// label's column is here.
+__device__ __forceinline__ void epilogue_loss_stats(const LossArgs& a, uint32_t tbase, int row, int n0) {
+  const bool in = row < a.M;
+  const int64_t label = in ? a.labels[row] : -1;
+  float m = -CUDART_INF_F, s = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < kFAccCols / 32; ++c) {
+    const int col = a.col0 + n0 + c * 32;
+    const int nv = a.vocab - col;       // columns of this chunk that exist
+    if (nv <= 0) break;                 // the same for the whole warp
+    uint32_t v[32];
+    __syncwarp();
+    tmem_ld_32x32b_x32(tbase + c * 32, v);
+    tmem_ld_wait();
+    float top = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < nv) top = fmaxf(top, __uint_as_float(v[i]));
+    const float nm = fmaxf(m, top);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < nv) sum += ex2((__uint_as_float(v[i]) - nm) * kLog2E);
+    s = (m == nm ? s : s * ex2((m - nm) * kLog2E)) + sum;
+    m = nm;
+    const int64_t at = label - col;
+    if (at >= 0 && at < 32 && at < nv) {
+      float l = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i == static_cast<int>(at)) l = __uint_as_float(v[i]);
+      a.label_logit[row] = l;
+    }
+  }
+  if (in) a.stats[static_cast<int64_t>(n0 / kFAccCols) * a.M + row] = make_float2(m, s);
+}
+
+// P = dloss (exp(l - lse) - onehot(label)) of this lane's row, bf16; zero in
+// the columns from `vocab` on and in rows whose label does not count.
+__device__ __forceinline__ void epilogue_loss_grad(const LossArgs& a, uint32_t tbase, int row, int n0) {
+  const bool in = row < a.M;
+  const int64_t label = in ? a.labels[row] : -1;
+  const bool counts = in && label != a.ignore_index && label >= 0 && label < a.vocab;
+  const float lse = in ? a.lse[row] : 0.0f;
+  const float d = counts ? a.dloss[row] : 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < kFAccCols / 32; ++c) {
+    if (n0 + c * 32 >= a.Nout) break;   // the same for the whole warp
+    const int col = a.col0 + n0 + c * 32;
+    const int nv = a.vocab - col;
+    const int64_t at = label - col;
+    uint32_t v[32];
+    __syncwarp();
+    tmem_ld_32x32b_x32(tbase + c * 32, v);
+    tmem_ld_wait();
+    if (in) {
+      float p[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float e = ex2((__uint_as_float(v[i]) - lse) * kLog2E);
+        p[i] = counts && i < nv ? d * (e - (i == at ? 1.0f : 0.0f)) : 0.0f;
+      }
+      store_bf16x32(a.out + static_cast<int64_t>(row) * a.Nout + n0 + c * 32, p);
+    }
+  }
+}
+
+// dX of one output column (this lane) over 32 rows, added to the pieces
+// before this one in fp32; the last piece rounds to bf16.
+__device__ __forceinline__ void epilogue_loss_dx(const LossArgs& a, const uint32_t (&v)[32], int col, int row0) {
+  if (col >= a.Nout || row0 >= a.M) return;
+  const int64_t ld = a.Nout;
+  const int64_t at = row0 * ld + col;
+  const int nrows = a.M - row0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (i < nrows) {
+      float x = __uint_as_float(v[i]);
+      if (!a.first) x += a.acc[at + i * ld];
+      if (a.last)
+        a.out[at + i * ld] = static_cast<uint16_t>(pack_bf16x2(x, 0.0f));
+      else
+        a.acc[at + i * ld] = x;
+    }
+  }
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(kFThreads, 1)
+    fused_nf4_gemm_kernel(const __grid_constant__ typename ModeTypes<kMode>::Maps maps,
+                          const typename ModeTypes<kMode>::Args args) {
+  constexpr bool kBwd = mode_transposed(kMode);
+  constexpr int kLora = mode_lora_steps(kMode);
+  constexpr int kTileCols = mode_tile_cols(kMode);
+  constexpr bool kLayer = kMode == kModeFwd || kMode == kModeBwd;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + kFAStages * kFA;
+  float* t8 = reinterpret_cast<float*>(sB + kFBStages * kFB);
+  uint64_t* full_a = reinterpret_cast<uint64_t*>(t8 + 256);
+  uint64_t* empty_a = full_a + kFAStages;
+  uint64_t* full_b = empty_a + kFAStages;
+  uint64_t* empty_b = full_b + kFBStages;
+  uint64_t* tfull = empty_b + kFBStages;
+  uint64_t* tempty = tfull + 1;   // [kFSlices]: one per accumulator
+  uint64_t* drain = tempty + kFSlices;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the pair is the cluster (2 x 1 x 1): rank 0 issues the MMAs
+  const int rank = static_cast<int>(blockIdx.x & 1);
+  const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
+  {
+    bool dq = args.sv.code8 != nullptr;
+    if constexpr (mode_gated(kMode)) dq = dq || args.sv2.code8 != nullptr;
+    if (dq) build_t8(t8);
+  }
+  if (threadIdx.x == 0) {
+    // Only CTA 0's full_a, full_b and tempty are waited on; every CTA's
+    // empty_a, empty_b and tfull receive the pair MMA's multicast commits.
+    for (int s = 0; s < kFAStages; ++s) {
+      mbar_init(&full_a[s], 1);            // CTA 0's producer, plus both CTAs' bytes
+      mbar_init(&empty_a[s], 1);
+    }
+    for (int s = 0; s < kFBStages; ++s) {
+      mbar_init(&full_b[s], 2 * kFDecWarps);   // both CTAs' decoder warps
+      mbar_init(&empty_b[s], 1);
+    }
+    mbar_init(tfull, 1);
+    for (int h = 0; h < kFSlices; ++h) mbar_init(&tempty[h], 2 * kFEpiWarps);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_holder, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  // the peer's barriers are initialised before any arrival reaches them
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const int num_tiles = args.m_tiles * args.n_tiles;
+  pdl_launch_dependents();   // after this CTA holds its TMEM
+  // the loss modes have no rank-r product before them: every input may come
+  // from the kernel that precedes
+  if constexpr (kLora == 0) pdl_wait();
+  // Otherwise no wait for the preceding kernel here.  It is always this library's
+  // rank-r product (Zc, or dZ), which lets this kernel launch only after all
+  // kernels before it have completed: the activations, the weights and the
+  // output buffer are final or free, and only the LoRA step's Zc (dZ) comes
+  // from the preceding kernel; the producer waits before loading it.
+
+  if (warp == 0) {
+    // ------------------------------ TMA producer ---------------------------
+    if (lane == 0) {
+      tma_prefetch_desc(&maps.act);
+      if constexpr (kLora > 0) {
+        tma_prefetch_desc(&maps.la);
+        tma_prefetch_desc(&maps.lb);
+      }
+      if constexpr (kLora > 1) {
+        if constexpr (kBwd) tma_prefetch_desc(&maps.act2);
+        tma_prefetch_desc(&maps.la2);
+        tma_prefetch_desc(&maps.lb2);
+      }
+      uint32_t ia = 0;                          // activation-ring slot counter
+      uint32_t last_parity[kFAStages];
+#pragma unroll
+      for (int s = 0; s < kFAStages; ++s) last_parity[s] = 2;
+      bool ok = true;
+      // take the next slot; CTA 0 arms its full barrier with both CTAs' bytes
+      auto take = [&](uint32_t& s_out, uint32_t bytes) -> bool {
+        const uint32_t s = ia % kFAStages, ph = (ia / kFAStages) & 1;
+        if (*abort_flag || !mbar_wait(&empty_a[s], ph ^ 1)) return false;
+        if (rank == 0) mbar_arrive_expect_tx(&full_a[s], 2 * bytes);
+        last_parity[s] = ph;
+        s_out = s;
+        ++ia;
+        return true;
+      };
+      auto bar0 = [&](uint32_t s) -> uint32_t { return mapa_shared(smem_u32(&full_a[s]), 0); };
+      // the activation rows of slice h of this CTA
+      auto act_row = [&](int m0, int h) -> int {
+        return kMode == kModeFwd ? m0 + 256 * rank + 128 * h : m0 + 256 * h + 128 * rank;
+      };
+      bool lora_ready = false;
+      for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+        const int m0 = (tile % args.m_tiles) * kFPairRows;
+        const int n0 = (tile / args.m_tiles) * kTileCols;
+        const int nh = tile_slices<kMode>(args.M, m0);
+        const uint32_t act_bytes = kLayer ? kFA : static_cast<uint32_t>(nh) * 16384u;
+        for (int kk = 0; kk < args.nk && ok; ++kk) {
+          uint32_t s;
+          if (!take(s, act_bytes)) { ok = false; break; }
+          uint8_t* a = sA + s * kFA;
+          const CUtensorMap* ma = &maps.act;
+          int kx = kk * 64;
+          if constexpr (kMode == kModeGatedBwd) {
+            if (kk >= args.nk / 2) {
+              ma = &maps.act2;
+              kx -= args.nk / 2 * 64;
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < kFSlices; ++h)
+            if (h < nh) tma_load_2d_pair(a + h * 16384, ma, bar0(s), kx, act_row(m0, h));
+        }
+        if (!ok) break;
+        // LoRA steps: Zc / dZ into one stage, B / A into the next
+        if (kLora > 0 && !lora_ready) {
+          pdl_wait();   // Zc (dZ) is the preceding kernel's output
+          lora_ready = true;
+        }
+        for (int l = 0; l < kLora && ok; ++l) {
+          const CUtensorMap *la = nullptr, *lb = nullptr;
+          if constexpr (kLora > 0) { la = &maps.la; lb = &maps.lb; }
+          if constexpr (kLora > 1) {
+            if (l == 1) { la = &maps.la2; lb = &maps.lb2; }
+          }
+          uint32_t s1, s2;
+          if (!take(s1, act_bytes)) { ok = false; break; }
+          uint8_t* a = sA + s1 * kFA;
+#pragma unroll
+          for (int h = 0; h < kFSlices; ++h)
+            if (h < nh) tma_load_2d_pair(a + h * 16384, la, bar0(s1), 0, act_row(m0, h));
+          if (!take(s2, kFB)) { ok = false; break; }
+          uint8_t* b = sA + s2 * kFA;
+          if (!kBwd) {
+            // B's columns of this CTA's half, two 64-column boxes (MN-major);
+            // gated: the CTA's own B in its step, rows past the end (zeros) in the other's
+            const int bx = kMode == kModeGatedFwd ? n0 : n0 + 128 * rank;
+            const int by = kMode == kModeGatedFwd && l != rank ? 64 : 0;
+#pragma unroll
+            for (int nb = 0; nb < kFBN / 64; ++nb)
+              tma_load_2d_pair(b + nb * 8192, lb, bar0(s2), bx + nb * 64, by);
+          } else {
+            // A's rows of this CTA's output columns (K-major)
+            tma_load_2d_pair(b, lb, bar0(s2), 0, n0 + 128 * rank);
+          }
+        }
+      }
+      if (!ok) *abort_flag = 1;
+      // CTA 0: let copies already in flight (its own and the peer's) land
+      // before either CTA can exit
+      if (rank == 0)
+        for (int s = 0; s < kFAStages; ++s)
+          if (last_parity[s] < 2) (void)mbar_wait(&full_a[s], last_parity[s]);
+    }
+  } else if (warp == 1) {
+    // ------------------------- MMA issuer (CTA 0 only) ----------------------
+    if (lane == 0 && rank == 0) {
+      // forward: D[m][n] += act[m][k] * Ŵtile[k][n] (tile MN-major, as B);
+      // backward: D[n][m] += Ŵtile[n][k] * dY[m][k] (tile K-major, as A)
+      constexpr uint32_t idesc = kBwd ? idesc_bf16_f32(256, kFAccCols, 0, 0)
+                                      : idesc_bf16_f32(256, kFAccCols, 0, 1);
+      uint32_t ia = 0, ib = 0, tc = 0;
+      bool ok = true;
+      auto wait_a = [&](uint32_t& s) -> bool {
+        s = ia % kFAStages;
+        const uint32_t ph = (ia / kFAStages) & 1;
+        ++ia;
+        return !*abort_flag && mbar_wait(&full_a[s], ph);
+      };
+      // one 16-wide K slice j of accumulator h: `w0` the weight operand
+      // (decoded tile, or B / A in the LoRA step), `a0` the activation stage
+      auto mma = [&](int h, uint32_t a0, uint32_t w0, int j, uint32_t accum) {
+        const uint64_t adesc = smem_desc(a0 + h * 16384 + j * 32, 16, 1024);
+        if (kBwd)
+          umma_bf16_pair(tmem + h * kFAccCols, smem_desc(w0 + j * 32, 16, 1024), adesc, idesc, accum);
+        else
+          umma_bf16_pair(tmem + h * kFAccCols, adesc, smem_desc(w0 + j * 2048, 8192, 1024), idesc,
+                         accum);
+      };
+      for (int tile = pair; tile < num_tiles && ok; tile += npairs, ++tc) {
+        const uint32_t tph = (tc & 1) ^ 1;       // parity of the previous tile's release
+        const int nh = tile_slices<kMode>(args.M, (tile % args.m_tiles) * kFPairRows);
+        for (int kk = 0; kk < args.nk; ++kk) {
+          uint32_t sa;
+          if (!wait_a(sa)) { ok = false; break; }
+          const uint32_t sb = ib % kFBStages, phb = (ib / kFBStages) & 1;
+          ++ib;
+          if (*abort_flag || !mbar_wait(&full_b[sb], phb)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(sA + sa * kFA), b0 = smem_u32(sB + sb * kFB);
+          const uint32_t acc = kk > 0 ? 1u : 0u;
+#pragma unroll
+          for (int h = 0; h < kFSlices; ++h) {
+            if (kk == 0) {   // first K-step of a tile: wait until this accumulator is drained
+              if (*abort_flag || !mbar_wait(&tempty[h], tph)) { ok = false; break; }
+              tc_fence_after();
+            }
+            if (kLayer || h < nh) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma(h, a0, b0, j, (acc || j > 0) ? 1u : 0u);
+            }
+          }
+          if (!ok) break;
+          umma_commit_pair_mc(&empty_a[sa], 0x3);
+          umma_commit_pair_mc(&empty_b[sb], 0x3);
+        }
+        if (!ok) break;
+        for (int l = 0; l < kLora; ++l) {   // LoRA steps
+          uint32_t s1, s2;
+          if (!wait_a(s1) || !wait_a(s2)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(sA + s1 * kFA), w0 = smem_u32(sA + s2 * kFA);
+          for (int j = 0; j < args.rsteps; ++j)
+#pragma unroll
+            for (int h = 0; h < kFSlices; ++h)
+              if (kLayer || h < nh) mma(h, a0, w0, j, 1u);
+          umma_commit_pair_mc(&empty_a[s1], 0x3);
+          umma_commit_pair_mc(&empty_a[s2], 0x3);
+        }
+        if (!ok) break;
+        umma_commit_pair_mc(tfull, 0x3);
+      }
+      if (!ok) *abort_flag = 1;
+      umma_commit_pair_mc(drain, 0x1);
+      (void)mbar_wait(drain, 0);
+    }
+  } else if (warp < 2 + kFDecAll) {
+    // ------------------------------ decoders -------------------------------
+    const int grp = (warp - 2) / kFDecWarps;   // this warp's turn among the groups
+    const int R = threadIdx.x - 64 - grp * kFBN;   // row of this CTA's decoded tile
+    // this CTA's weight (the gated forward's CTA 1 has the second one)
+    const ScaleView* sv1 = &args.sv;
+    if constexpr (kMode == kModeGatedFwd) {
+      if (rank != 0) sv1 = &args.sv2;
+    }
+    const float off1 = sv1->code8 != nullptr ? __ldg(sv1->offset) : 0.0f;
+    float off2 = 0.0f;
+    if constexpr (kMode == kModeGatedBwd) {
+      if (args.sv2.code8 != nullptr) off2 = __ldg(args.sv2.offset);
+    }
+    const int nsteps = args.nk;                // decoded steps per tile
+    bool ok = true;
+    int tile = pair, kk = 0;                   // the step being decoded
+    advance(tile, kk, grp, nsteps, npairs);
+    int ptile = tile, pkk = kk;                // the step being prefetched
+    uint32_t ib = static_cast<uint32_t>(grp);
+    // One K-step: wait for a free weight stage, decode this thread's row.
+    auto step = [&](const RowFetch& f) {
+      const uint32_t s = ib % kFBStages, ph = (ib / kFBStages) & 1;
+      if (*abort_flag || !mbar_wait(&empty_b[s], ph ^ 1)) {
+        ok = false;
+        return;
+      }
+      uint8_t* brow = sB + s * kFB + R * 128;
+      const uint32_t sw = static_cast<uint32_t>(R & 7);
+      if (f.valid) {
+        const ScaleView* sv = sv1;
+        float off = off1;
+        if constexpr (kMode == kModeGatedBwd) {
+          if (f.second) { sv = &args.sv2; off = off2; }
+        }
+        const float a = sv->code8 == nullptr
+                            ? f.absv
+                            : __fadd_rn(__fmul_rn(t8[f.q], f.s2v), off);
+        uint32_t H[4], L[4];
+        build_lut(kNF4g + 16 * sv->codebook, a, H, L);
+        const uint32_t pw[8] = {f.p0.x, f.p0.y, f.p0.z, f.p0.w, f.p1.x, f.p1.y, f.p1.z, f.p1.w};
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(brow + ((static_cast<uint32_t>(c) ^ sw) << 4)) =
+              decode8(pw[c], H, L);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(brow + ((static_cast<uint32_t>(c) ^ sw) << 4)) =
+              make_uint4(0, 0, 0, 0);
+      }
+      // the rows are visible to the tensor core (async proxy), then CTA 0's
+      // barrier of the stage counts this warp
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full_b[s]), 0));
+      advance(tile, kk, kFDecGroups, nsteps, npairs);
+      ib += kFDecGroups;
+    };
+    // Three prefetch slots consumed and refilled in place (no register moves
+    // that would wait on loads still in flight).
+    RowFetch q0 = fetch_row<kMode>(args, ptile, pkk, R, rank, num_tiles);
+    advance(ptile, pkk, kFDecGroups, nsteps, npairs);
+    RowFetch q1 = fetch_row<kMode>(args, ptile, pkk, R, rank, num_tiles);
+    advance(ptile, pkk, kFDecGroups, nsteps, npairs);
+    RowFetch q2 = fetch_row<kMode>(args, ptile, pkk, R, rank, num_tiles);
+    advance(ptile, pkk, kFDecGroups, nsteps, npairs);
+    while (ok && tile < num_tiles) {
+      step(q0);
+      q0 = fetch_row<kMode>(args, ptile, pkk, R, rank, num_tiles);
+      advance(ptile, pkk, kFDecGroups, nsteps, npairs);
+      if (!ok || tile >= num_tiles) break;
+      step(q1);
+      q1 = fetch_row<kMode>(args, ptile, pkk, R, rank, num_tiles);
+      advance(ptile, pkk, kFDecGroups, nsteps, npairs);
+      if (!ok || tile >= num_tiles) break;
+      step(q2);
+      q2 = fetch_row<kMode>(args, ptile, pkk, R, rank, num_tiles);
+      advance(ptile, pkk, kFDecGroups, nsteps, npairs);
+    }
+    if (!ok) *abort_flag = 1;
+  } else {
+    // ------------------------------ epilogue -------------------------------
+    const int q = warp & 3;
+    uint32_t tc = 0;
+    bool ok = true;
+    const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);   // CTA 0's release barriers
+    for (int tile = pair; tile < num_tiles && ok; tile += npairs, ++tc) {
+      const int m0 = (tile % args.m_tiles) * kFPairRows;
+      const int n0 = (tile / args.m_tiles) * kTileCols;
+      const int nh = tile_slices<kMode>(args.M, m0);
+      if (*abort_flag || !mbar_wait(tfull, tc & 1)) { ok = false; break; }
+      tc_fence_after();
+      const int64_t ld = args.Nout;
+#pragma unroll 1
+      for (int h = 0; h < kFSlices; ++h) {
+        const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * kFAccCols;
+        if constexpr (kMode == kModeGatedFwd) {
+          if (h < nh) epilogue_gated(args, tbase, m0 + 256 * h + 128 * rank + q * 32 + lane, n0);
+        } else if constexpr (kMode == kModeLossStats) {
+          if (h < nh)
+            epilogue_loss_stats(args, tbase, m0 + 256 * h + 128 * rank + q * 32 + lane, n0);
+        } else if constexpr (kMode == kModeLossGrad) {
+          if (h < nh)
+            epilogue_loss_grad(args, tbase, m0 + 256 * h + 128 * rank + q * 32 + lane, n0);
+        } else
+#pragma unroll 1
+        for (int c = 0; c < kFAccCols / 32; ++c) {
+          if (!kLayer && h >= nh) break;
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tbase + c * 32, v);
+          tmem_ld_wait();
+          if constexpr (kMode == kModeLossDX) {
+            epilogue_loss_dx(args, v, n0 + 128 * rank + q * 32 + lane, m0 + h * kFAccCols + c * 32);
+          } else if (!kBwd) {
+            // lane = output row, 32 consecutive output columns
+            const int row = m0 + 256 * rank + h * 128 + q * 32 + lane;
+            const int col = n0 + c * 32;
+            if (row < args.M && col < args.Nout) {
+              uint4* dst = reinterpret_cast<uint4*>(args.out + row * ld + col);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dst[i] = make_uint4(
+                    pack_bf16x2(__uint_as_float(v[8 * i + 0]), __uint_as_float(v[8 * i + 1])),
+                    pack_bf16x2(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3])),
+                    pack_bf16x2(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5])),
+                    pack_bf16x2(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7])));
+            }
+          } else {
+            // lane = output column, 32 consecutive output rows
+            const int col = n0 + 128 * rank + q * 32 + lane;
+            const int row0 = m0 + h * kFAccCols + c * 32;
+            if (col < args.Nout && row0 < args.M) {
+              uint16_t* dst = args.out + row0 * ld + col;
+              const int nrows = args.M - row0;   // rows left in the output (>= 1)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const uint32_t pr = pack_bf16x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                if (i < nrows) dst[i * ld] = static_cast<uint16_t>(pr);
+                if (i + 1 < nrows) dst[(i + 1) * ld] = static_cast<uint16_t>(pr >> 16);
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(h) * 8u);
+      }
+    }
+    if (!ok) *abort_flag = 1;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // neither CTA leaves while the pair MMA, the peer's copies or the peer's
+  // arrivals may still reach it
+  cluster_sync_all();
+  if (*abort_flag && threadIdx.x == 0) raise_status(args.d_status, QLORA_ERR_TIMEOUT);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int kMode>
+cudaError_t set_fused_attr() {
+  static DeviceOnce once;
+  return once.run([](int) {
+    return cudaFuncSetAttribute(fused_nf4_gemm_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kFSmem));
+  });
+}
+
+}  // namespace
+}  // namespace qnf4

@@ -1,0 +1,338 @@
+// The gated block over two NF4 frozen-base weights with LoRA adapters:
+//
+//   g = X·Ŵg + Zg·Bg,  u = X·Ŵu + Zu·Bu,  H = act(g) * u,   Z = bf16(c·X·A)
+//   dG = dH * u * act'(g),  dU = dH * act(g),  dZ = bf16(c·d·Bᵀ),
+//   dX = dG·Ŵgᵀ + dU·Ŵuᵀ + dZg·Agᵀ + dZu·Auᵀ,  dA = Xᵀ·dZ,  dB = Zᵀ·d
+//
+// Forward: the rank-r products of both adapters in one launch, then one fused
+// GEMM over both weights whose epilogue forms H (and keeps g and u, in bf16 or
+// in 8 bits).  Backward: one pass over dH, g and u for dG and dU, both dZ in
+// one launch, one fused GEMM over both weights for dX, and beside it both dA
+// and both dB in a launch each.
+#include <mutex>
+
+#include "act.cuh"
+#include "common.cuh"
+#include "fused.cuh"
+#include "kernels.cuh"
+#include "profile.cuh"
+#include "rank.cuh"
+#include "tmap.cuh"
+
+namespace qnf4 {
+namespace {
+
+// dG and dU of eight elements a thread.  kG8: g and u come as 8-bit
+// checkpoints.  Streams 3 (or 2 1/32 ·2 B...) reads and 2 writes of M x N: HBM-bound.
+template <bool kG8>
+__global__ void __launch_bounds__(256)
+    gated_grad_kernel(const uint4* __restrict__ dH, const void* __restrict__ G, const void* __restrict__ U,
+                      const float* __restrict__ Gs, const float* __restrict__ Us, int64_t pieces, int act,
+                      uint4* __restrict__ dG, uint4* __restrict__ dU) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < pieces; i += stride) {
+    const uint4 h4 = __ldcs(dH + i);
+    float g[8], u[8];
+    if constexpr (kG8) {
+      const uint2 g2 = __ldcs(static_cast<const uint2*>(G) + i), u2 = __ldcs(static_cast<const uint2*>(U) + i);
+      const float sg = __ldg(Gs + (i >> 3)), su = __ldg(Us + (i >> 3));
+      const uint32_t gw[2] = {g2.x, g2.y}, uw[2] = {u2.x, u2.y};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        g[k] = round_bf16(act8_value(static_cast<int8_t>(gw[k >> 2] >> (8 * (k & 3))), sg));
+        u[k] = round_bf16(act8_value(static_cast<int8_t>(uw[k >> 2] >> (8 * (k & 3))), su));
+      }
+    } else {
+      const uint4 g4 = __ldcs(static_cast<const uint4*>(G) + i), u4 = __ldcs(static_cast<const uint4*>(U) + i);
+      const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        g[2 * k] = __uint_as_float(gw[k] << 16);
+        g[2 * k + 1] = __uint_as_float(gw[k] & 0xFFFF0000u);
+        u[2 * k] = __uint_as_float(uw[k] << 16);
+        u[2 * k + 1] = __uint_as_float(uw[k] & 0xFFFF0000u);
+      }
+    }
+    const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w};
+    uint32_t og[4], ou[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float d0, d1;
+      const float h0 = __uint_as_float(hw[k] << 16), h1 = __uint_as_float(hw[k] & 0xFFFF0000u);
+      const float a0 = act_value_grad(act, g[2 * k], d0), a1 = act_value_grad(act, g[2 * k + 1], d1);
+      og[k] = pack_bf16x2(h0 * u[2 * k] * d0, h1 * u[2 * k + 1] * d1);
+      ou[k] = pack_bf16x2(h0 * a0, h1 * a1);
+    }
+    dG[i] = make_uint4(og[0], og[1], og[2], og[3]);
+    dU[i] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+  }
+}
+
+// Two rank-r contractions in one launch (see run_skinny for the modes).
+template <bool kAmn, bool kBmn>
+cudaError_t run_skinny_two(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ta2,
+                           const CUtensorMap& tb2, int Mp, int Kp, int ncols, float scale, int mode,
+                           void* out, void* out_second, int ld, int32_t* d_status, cudaStream_t st,
+                           int nout, uint16_t* pad = nullptr, uint16_t* pad_second = nullptr, int ld2 = 0) {
+  SkinnyArgs a{};
+  a.Mp = Mp;
+  a.ncols = ncols;
+  a.nout = nout;
+  a.scale = scale;
+  a.mode = mode;
+  a.out = out;
+  a.ld = ld;
+  a.out2 = pad;
+  a.ld2 = ld2;
+  a.d_status = d_status;
+  // half of the sizing SM count for each of the two
+  const int splits = skinny_splits(Mp, (Kp + 63) / 64, g_ws_sms / 2);
+  return launch_skinny<kAmn, kBmn, true, false>(SkinnyMaps<true, false>{ta, tb, ta2, tb2}, a, Kp, splits,
+                                                SkinnySecond{out_second, pad_second}, SkinnyA8{}, st);
+}
+
+int tiles_of(int64_t n, int per) { return static_cast<int>((n + per - 1) / per); }
+
+}  // namespace
+
+size_t gated_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r) {
+  (void)N;
+  const int rp = padded_rank(r);
+  // Zg and Zu (a copy padded to rp columns where the caller keeps them with r),
+  // and both A padded to rp columns when r is not a multiple of 8
+  return 2 * align256(static_cast<size_t>(M) * rp * 2) +
+         (rp != r ? 2 * align256(static_cast<size_t>(K) * rp * 2) : 0);
+}
+
+size_t gated_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r) {
+  const int rp = padded_rank(r);
+  // dG, dU; dZg, dZu; when r is not a multiple of 8 padded copies of Zg, Zu, Ag, Au
+  return 2 * align256(static_cast<size_t>(M) * N * 2) + 2 * align256(static_cast<size_t>(M) * rp * 2) +
+         (rp != r ? 2 * align256(static_cast<size_t>(M) * rp * 2) + 2 * align256(static_cast<size_t>(K) * rp * 2)
+                  : 0);
+}
+
+cudaError_t launch_gated_fwd(int64_t M, int64_t K, int64_t N, int r, const uint16_t* X,
+                             const GatedWeights& w, uint16_t* H, const GatedKept& kept, void* ws,
+                             size_t ws_bytes, int32_t* d_status, cudaStream_t st, int num_sms) {
+  (void)num_sms;
+  WsCursor cur{static_cast<char*>(ws), ws_bytes};
+  const int rp = padded_rank(r);
+  const bool pad = rp != r;
+  const int iM = static_cast<int>(M), iK = static_cast<int>(K);
+  uint16_t* Zwg = static_cast<uint16_t*>(cur.take(static_cast<size_t>(M) * rp * 2));
+  uint16_t* Zwu = static_cast<uint16_t*>(cur.take(static_cast<size_t>(M) * rp * 2));
+  uint16_t* Apg = pad ? static_cast<uint16_t*>(cur.take(static_cast<size_t>(K) * rp * 2)) : nullptr;
+  uint16_t* Apu = pad ? static_cast<uint16_t*>(cur.take(static_cast<size_t>(K) * rp * 2)) : nullptr;
+  if (!cur.ok) return cudaErrorInvalidValue;
+  cudaError_t e = cudaSuccess;
+  const uint16_t *Ag = w.Ag, *Au = w.Au;
+  if (pad) {
+    e = launch_pad(w.Ag, K, r, Apg, rp, st);
+    if (e == cudaSuccess) e = launch_pad(w.Au, K, r, Apu, rp, st);
+    if (e != cudaSuccess) return e;
+    Ag = Apg;
+    Au = Apu;
+  }
+  // Z: into the kept buffers (M x r) when there are, with a copy of row pitch
+  // rp for the fused kernel's TMA where r is not a multiple of 8
+  const bool keep = kept.Zg != nullptr;
+  uint16_t *Zg = keep ? kept.Zg : Zwg, *Zu = keep ? kept.Zu : Zwu;
+  const bool copy = keep && pad;
+  CUtensorMap tX, tAg, tAu;
+  if (!make_tmap_2d(&tX, X, kBF16, 2, M, K, K, 64, 128, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&tAg, Ag, kBF16, 2, K, rp, rp, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&tAu, Au, kBF16, 2, K, rp, rp, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  e = run_skinny_two<false, true>(tX, tAg, tX, tAu, iM, iK, rp, w.c, 0, Zg, Zu, keep ? r : rp, d_status, st,
+                                  keep ? r : rp, copy ? Zwg : nullptr, copy ? Zwu : nullptr, rp);
+  if (e != cudaSuccess) return e;
+  e = set_fused_attr<kModeGatedFwd>();
+  if (e != cudaSuccess) return e;
+  ModeTypes<kModeGatedFwd>::Maps maps;
+  maps.act = tX;
+  maps.act2 = tX;
+  if (!make_tmap_2d(&maps.la, copy ? Zwg : Zg, kBF16, 2, M, rp, rp, 64, 128, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&maps.la2, copy ? Zwu : Zu, kBF16, 2, M, rp, rp, 64, 128, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&maps.lb, w.Bg, kBF16, 2, r, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&maps.lb2, w.Bu, kBF16, 2, r, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  GatedArgs ga{};
+  ga.M = iM;
+  ga.Nout = static_cast<int>(N);
+  ga.Nw = static_cast<int>(N);
+  ga.nk = static_cast<int>(K / 64);
+  ga.rsteps = rsteps_of(r);
+  ga.m_tiles = tiles_of(M, kFPairRows);
+  ga.n_tiles = tiles_of(N, mode_tile_cols(kModeGatedFwd));
+  ga.sv = w.sv_g;
+  ga.packed = w.packed_g;
+  ga.sv2 = w.sv_u;
+  ga.packed2 = w.packed_u;
+  ga.out = H;
+  ga.act = w.act;
+  ga.G = kept.G;
+  ga.U = kept.U;
+  ga.G8 = kept.G8;
+  ga.U8 = kept.U8;
+  ga.Gs = kept.Gs;
+  ga.Us = kept.Us;
+  ga.d_status = d_status;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int grid = fused_pairs(ga.m_tiles * ga.n_tiles, sms);
+  {
+    ProfScope prof(kProfGated, st);
+    e = launch_pdl_pair(fused_nf4_gemm_kernel<kModeGatedFwd>, dim3(2 * grid), dim3(kFThreads), kFSmem, st,
+                        maps, ga);
+  }
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint16_t* dH,
+                             const uint16_t* X, const int8_t* X8, const float* X8_scales,
+                             const GatedWeights& w, const GatedKept& kept, uint16_t* dX, void* dAg,
+                             void* dBg, void* dAu, void* dBu, bool grad_bf16, void* ws,
+                             size_t ws_bytes, int32_t* d_status, cudaStream_t st, int num_sms) {
+  WsCursor cur{static_cast<char*>(ws), ws_bytes};
+  const int rp = padded_rank(r);
+  const bool pad = rp != r;
+  const int iM = static_cast<int>(M), iK = static_cast<int>(K), iN = static_cast<int>(N);
+  auto bf16_rows = [&](int64_t rows, int64_t cols) {
+    return static_cast<uint16_t*>(cur.take(static_cast<size_t>(rows) * cols * 2));
+  };
+  uint16_t *dG = bf16_rows(M, N), *dU = bf16_rows(M, N);
+  uint16_t *dZg = bf16_rows(M, rp), *dZu = bf16_rows(M, rp);
+  uint16_t *Zpg = nullptr, *Zpu = nullptr, *Apg = nullptr, *Apu = nullptr;
+  if (pad) {
+    Zpg = bf16_rows(M, rp);
+    Zpu = bf16_rows(M, rp);
+    Apg = bf16_rows(K, rp);
+    Apu = bf16_rows(K, rp);
+  }
+  if (!cur.ok) return cudaErrorInvalidValue;
+  cudaError_t e = cudaSuccess;
+  const uint16_t *Ag = w.Ag, *Au = w.Au, *Zg = kept.Zg, *Zu = kept.Zu;
+  if (pad) {
+    e = launch_pad(w.Ag, K, r, Apg, rp, st);
+    if (e == cudaSuccess) e = launch_pad(w.Au, K, r, Apu, rp, st);
+    if (e == cudaSuccess) e = launch_pad(kept.Zg, M, r, Zpg, rp, st);
+    if (e == cudaSuccess) e = launch_pad(kept.Zu, M, r, Zpu, rp, st);
+    if (e != cudaSuccess) return e;
+    Ag = Apg;
+    Au = Apu;
+    Zg = Zpg;
+    Zu = Zpu;
+  }
+  // dG, dU
+  {
+    const int64_t pieces = M * N / 8;
+    const int64_t want = (pieces + 255) / 256, most = static_cast<int64_t>(num_sms) * 8;
+    const dim3 grid(static_cast<unsigned>(want < most ? want : most));
+    ProfScope prof(kProfGated, st);
+    const bool g8 = kept.G8 != nullptr;
+    e = launch_pdl(g8 ? gated_grad_kernel<true> : gated_grad_kernel<false>, grid, dim3(256), 0, st, 1,
+                   reinterpret_cast<const uint4*>(dH),
+                   g8 ? static_cast<const void*>(kept.G8) : static_cast<const void*>(kept.G),
+                   g8 ? static_cast<const void*>(kept.U8) : static_cast<const void*>(kept.U),
+                   static_cast<const float*>(kept.Gs), static_cast<const float*>(kept.Us), pieces, w.act,
+                   reinterpret_cast<uint4*>(dG), reinterpret_cast<uint4*>(dU));
+  }
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // dZ = bf16(c d Bᵀ), both (columns past r are zero: B's rows past r arrive as zero fill)
+  CUtensorMap tG, tU, tBg, tBu;
+  if (!make_tmap_2d(&tG, dG, kBF16, 2, M, N, N, 64, 128, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&tU, dU, kBF16, 2, M, N, N, 64, 128, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&tBg, w.Bg, kBF16, 2, r, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&tBu, w.Bu, kBF16, 2, r, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  e = run_skinny_two<false, false>(tG, tBg, tU, tBu, iM, iN, rp, w.c, 0, dZg, dZu, rp, d_status, st, rp);
+  if (e != cudaSuccess) return e;
+  // dX over both weights
+  e = set_fused_attr<kModeGatedBwd>();
+  if (e != cudaSuccess) return e;
+  ModeTypes<kModeGatedBwd>::Maps maps;
+  maps.act = tG;
+  maps.act2 = tU;
+  if (!make_tmap_2d(&maps.la, dZg, kBF16, 2, M, rp, rp, 64, 128, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&maps.la2, dZu, kBF16, 2, M, rp, rp, 64, 128, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&maps.lb, Ag, kBF16, 2, K, rp, rp, 64, kFBN, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&maps.lb2, Au, kBF16, 2, K, rp, rp, 64, kFBN, kSW128)) return cudaErrorInvalidValue;
+  GatedArgs ga{};
+  ga.M = iM;
+  ga.Nout = iK;
+  ga.Nw = iN;
+  ga.nk = static_cast<int>(2 * (N / 64));
+  ga.rsteps = rsteps_of(r);
+  ga.m_tiles = tiles_of(M, kFPairRows);
+  ga.n_tiles = tiles_of(K, mode_tile_cols(kModeGatedBwd));
+  ga.sv = w.sv_g;
+  ga.packed = w.packed_g;
+  ga.sv2 = w.sv_u;
+  ga.packed2 = w.packed_u;
+  ga.out = dX;
+  ga.d_status = d_status;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int grid = fused_pairs(ga.m_tiles * ga.n_tiles, sms);
+  // operands of dA and dB, read transposed
+  CUtensorMap tXmn, tdZg, tdZu, tGmn, tUmn, tZg, tZu;
+  if (X8 == nullptr && !make_tmap_2d(&tXmn, X, kBF16, 2, M, K, K, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&tdZg, dZg, kBF16, 2, M, rp, rp, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&tdZu, dZu, kBF16, 2, M, rp, rp, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&tGmn, dG, kBF16, 2, M, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&tUmn, dU, kBF16, 2, M, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&tZg, Zg, kBF16, 2, M, rp, rp, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&tZu, Zu, kBF16, 2, M, rp, rp, 64, 64, kSW128)) return cudaErrorInvalidValue;
+
+  // dX first, then dA and dB (which need only dZ, Z, X, dG and dU) on the
+  // library's stream, so that they take the SMs dX leaves idle; the caller's
+  // stream waits for them before the call returns.
+  std::lock_guard<std::mutex> lock(g_side_mu);
+  SideStream* ss = prof_timing(kProfSkinny) ? nullptr : side_stream(dev);
+  cudaStream_t s2 = st;
+  if (ss != nullptr && cudaEventRecord(ss->fork, st) == cudaSuccess) s2 = ss->s;
+  {
+    ProfScope prof(kProfGated, st);
+    e = launch_pdl_pair(fused_nf4_gemm_kernel<kModeGatedBwd>, dim3(2 * grid), dim3(kFThreads), kFSmem, st,
+                        maps, ga);
+  }
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (s2 != st) {
+    const cudaError_t ew = cudaStreamWaitEvent(s2, ss->fork, 0);
+    if (ew != cudaSuccess) {
+      s2 = st;   // no fork: dA and dB after dX on the caller's stream
+      if (e == cudaSuccess) e = ew;
+    }
+  }
+  if (e == cudaSuccess && X8 != nullptr) {
+    SkinnyArgs sa{};
+    sa.Mp = iK;
+    sa.ncols = sa.nout = sa.ld = r;
+    sa.scale = 1.0f;
+    sa.mode = grad_bf16 ? 0 : 1;
+    sa.out = dAg;
+    sa.d_status = d_status;
+    e = launch_skinny<true, true, true, true>(SkinnyMaps<true, true>{tdZg, tdZu}, sa, iM,
+                                              skinny_splits(iK, (iM + 63) / 64, g_ws_sms / 2),
+                                              SkinnySecond{dAu, nullptr}, SkinnyA8{X8, X8_scales, iM, iK}, s2);
+  } else if (e == cudaSuccess) {
+    e = run_skinny_two<true, true>(tXmn, tdZg, tXmn, tdZu, iK, iM, r, 1.0f, grad_bf16 ? 0 : 1, dAg, dAu, r,
+                                   d_status, s2, r);
+  }
+  if (e == cudaSuccess)
+    e = run_skinny_two<true, true>(tGmn, tZg, tUmn, tZu, iN, iM, r, 1.0f, grad_bf16 ? 3 : 2, dBg, dBu, r,
+                                   d_status, s2, r);
+  if (s2 != st) {
+    // always join, so that nothing on st can run ahead of work already queued
+    const cudaError_t ej = cudaEventRecord(ss->join, s2);
+    const cudaError_t ew = ej == cudaSuccess ? cudaStreamWaitEvent(st, ss->join, 0) : ej;
+    if (e == cudaSuccess) e = ew;
+  }
+  return e;
+}
+
+}  // namespace qnf4

@@ -159,6 +159,16 @@ cudaError_t launch_gemv(int64_t M, int64_t K, int64_t N, int r, const uint16_t* 
                         const uint16_t* B, float c, uint16_t* Y, uint16_t* Zc, int ldz,
                         bool zc_only, int32_t* d_status, cudaStream_t st, int num_sms);
 
+// linear.cu — a library-owned stream per device for work beside the caller's
+// stream (null if it cannot be created).  g_side_mu is held from a fork to its
+// join.
+struct SideStream {
+  cudaStream_t s = nullptr;
+  cudaEvent_t fork = nullptr, join = nullptr;
+};
+extern std::mutex g_side_mu;
+SideStream* side_stream(int dev);
+
 // linear.cu — forward and backward of the layer
 size_t linear_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r);
 size_t linear_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r);
@@ -169,7 +179,55 @@ cudaError_t launch_linear_fwd(int64_t M, int64_t K, int64_t N, int r, const uint
 cudaError_t launch_linear_bwd(int64_t M, int64_t K, int64_t N, int r, const uint16_t* dY,
                               const uint16_t* X, const uint16_t* Zc, const uint8_t* packed,
                               ScaleView sv, const uint16_t* A, const uint16_t* B, float c,
-                              uint16_t* dX, float* dA, float* dB, void* ws, size_t ws_bytes,
-                              int32_t* d_status, cudaStream_t st, int num_sms);
+                              uint16_t* dX, void* dA, void* dB, void* ws, size_t ws_bytes,
+                              int32_t* d_status, cudaStream_t st, int num_sms, bool grad_bf16 = false,
+                              const int8_t* X8 = nullptr, const float* X8_scales = nullptr);
+// (dA, dB are fp32, or bf16 with grad_bf16; with X8 the layer's input is an
+// 8-bit checkpoint, X is null and Zc is not)
+
+// act8.cu — 8-bit activation checkpoints
+cudaError_t launch_act8_quantize(const uint16_t* X, int64_t numel, int8_t* codes, float* scales,
+                                 int32_t* d_status, cudaStream_t st, int num_sms);
+cudaError_t launch_act8_dequantize(const int8_t* codes, const float* scales, int64_t numel, uint16_t* X,
+                                   cudaStream_t st, int num_sms);
+
+// gated.cu — the gated block over two weights
+struct GatedWeights {
+  const uint8_t *packed_g, *packed_u;
+  ScaleView sv_g, sv_u;
+  const uint16_t *Ag, *Bg, *Au, *Bu;
+  float c;
+  int act;
+};
+// What the forward keeps for the backward: g and u in bf16 (G, U) or in 8 bits
+// (G8, Gs, U8, Us), and the rank-r products; all null when nothing is kept.
+struct GatedKept {
+  uint16_t *G, *U;
+  int8_t *G8, *U8;
+  float *Gs, *Us;
+  uint16_t *Zg, *Zu;
+};
+size_t gated_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r);
+size_t gated_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r);
+cudaError_t launch_gated_fwd(int64_t M, int64_t K, int64_t N, int r, const uint16_t* X,
+                             const GatedWeights& w, uint16_t* H, const GatedKept& kept, void* ws,
+                             size_t ws_bytes, int32_t* d_status, cudaStream_t st, int num_sms);
+cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint16_t* dH,
+                             const uint16_t* X, const int8_t* X8, const float* X8_scales,
+                             const GatedWeights& w, const GatedKept& kept, uint16_t* dX, void* dAg,
+                             void* dBg, void* dAu, void* dBu, bool grad_bf16, void* ws,
+                             size_t ws_bytes, int32_t* d_status, cudaStream_t st, int num_sms);
+
+// loss.cu — softmax cross entropy behind an NF4 head
+size_t loss_fwd_workspace_bytes(int64_t M, int64_t N);
+size_t loss_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N);
+cudaError_t launch_loss_fwd(int64_t M, int64_t K, int64_t N, int64_t vocab, const uint16_t* X,
+                            const uint8_t* packed, ScaleView sv, const int64_t* labels,
+                            int64_t ignore_index, float* loss, float* lse, void* ws, size_t ws_bytes,
+                            int32_t* d_status, cudaStream_t st, int num_sms);
+cudaError_t launch_loss_bwd(int64_t M, int64_t K, int64_t N, int64_t vocab, const float* dloss,
+                            const uint16_t* X, const float* lse, const uint8_t* packed, ScaleView sv,
+                            const int64_t* labels, int64_t ignore_index, uint16_t* dX, void* ws,
+                            size_t ws_bytes, int32_t* d_status, cudaStream_t st, int num_sms);
 
 }  // namespace qnf4

@@ -15,7 +15,10 @@ enum ProfKind {
   kProfDequantize = 4,
   kProfGemv = 5,
   kProfOther = 6,
-  kProfKinds = 7
+  kProfAct8 = 7,
+  kProfGated = 8,
+  kProfLoss = 9,
+  kProfKinds = 10
 };
 
 // Counts one launch of kind `id` and, while profiling is enabled, brackets it

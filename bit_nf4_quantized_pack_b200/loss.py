@@ -1,0 +1,80 @@
+"""Softmax cross entropy behind an NF4 frozen head, the logits never in memory
+(``qlora_head_loss_*`` in ``include/qlora_nf4.h``):
+
+    l = X·Ŵ,  lse = log Σ exp(l),  loss = lse - l[label]
+    dX = dloss · (softmax(l) - onehot(label)) · Ŵᵀ
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import _args
+from ._lib import check, lib
+
+__all__ = ["head_loss_forward", "head_loss_backward"]
+
+
+def _head(X, w, labels, vocab):
+    M, K, dev = _args.cuda_2d(X, "X")
+    N = w.shape[1] if len(w.shape) == 2 else -1
+    _args.weight(w, "w", (K, N), dev)
+    _args.tensor(labels, "labels", (M,), dev, torch.int64)
+    vocab = N if vocab is None else int(vocab)
+    if not 1 <= vocab <= N:
+        raise ValueError(f"vocab must be 1 .. {N}, not {vocab}")
+    return M, K, N, vocab, dev
+
+
+def head_loss_forward(X, w, labels, *, vocab: int | None = None, ignore_index: int = -100, loss=None,
+                      lse=None, status=None, workspace=None):
+    """Per-row losses and log-sum-exps (fp32, M each) of the logits X·Ŵ.
+
+    w is the K x N ``NF4Weight`` of the head; its columns from ``vocab`` on (all
+    N by default) are padding.  Rows whose label is ``ignore_index`` have loss
+    0; any other label outside 0 .. vocab - 1 is a device error."""
+    from . import _finish, new_status
+    M, K, N, vocab, dev = _head(X, w, labels, vocab)
+    with torch.cuda.device(dev):
+        out = []
+        for t, name in ((loss, "loss"), (lse, "lse")):
+            if t is None:
+                t = torch.empty((M,), dtype=torch.float32, device=dev)
+            else:
+                _args.tensor(t, name, (M,), dev, torch.float32)
+            out.append(t)
+        need = lib.qlora_head_loss_fwd_workspace_size(M, K, N)
+        ws = _args.workspace(workspace, need, dev)
+        own = status is None
+        status = new_status(dev) if own else status
+        check(lib.qlora_head_loss_fwd(M, K, N, vocab, X.data_ptr(), C.byref(w.cstruct()), labels.data_ptr(),
+                                      int(ignore_index), out[0].data_ptr(), out[1].data_ptr(), ws.data_ptr(),
+                                      ws.numel(), status.data_ptr(), _args.stream()), "qlora_head_loss_fwd")
+        _finish(status, own, "qlora_head_loss_fwd")
+    return tuple(out)
+
+
+def head_loss_backward(dloss, X, lse, w, labels, *, vocab: int | None = None, ignore_index: int = -100,
+                       dX=None, status=None, workspace=None):
+    """dX (bf16 M x K) from dloss (fp32 M, the gradient of each row's loss: 1/count
+    for the mean over count labels) and the forward's lse."""
+    from . import _finish, new_status
+    M, K, N, vocab, dev = _head(X, w, labels, vocab)
+    _args.tensor(dloss, "dloss", (M,), dev, torch.float32)
+    _args.tensor(lse, "lse", (M,), dev, torch.float32)
+    with torch.cuda.device(dev):
+        if dX is None:
+            dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        else:
+            _args.tensor(dX, "dX", (M, K), dev)
+        need = lib.qlora_head_loss_bwd_workspace_size(M, K, N)
+        ws = _args.workspace(workspace, need, dev)
+        own = status is None
+        status = new_status(dev) if own else status
+        check(lib.qlora_head_loss_bwd(M, K, N, vocab, dloss.data_ptr(), X.data_ptr(), lse.data_ptr(),
+                                      C.byref(w.cstruct()), labels.data_ptr(), int(ignore_index),
+                                      dX.data_ptr(), ws.data_ptr(), ws.numel(), status.data_ptr(),
+                                      _args.stream()), "qlora_head_loss_bwd")
+        _finish(status, own, "qlora_head_loss_bwd")
+    return dX

@@ -100,6 +100,12 @@ typedef struct qlora_nf4_state {
   float*   offset;
 } qlora_nf4_state;
 
+/* Activation of the gated block (qlora_gated_fwd): x·sigmoid(x), or the tanh
+ * form of the Gaussian error linear unit. */
+typedef int32_t qlora_act;
+#define QLORA_ACT_SILU 0
+#define QLORA_ACT_GELU 1
+
 /* ABI version of this header (bumped on any incompatible change). */
 #define QLORA_NF4_ABI_VERSION 2
 int32_t qlora_abi_version(void);
@@ -312,6 +318,132 @@ qlora_status qlora_linear_bwd(int64_t M, int64_t K, int64_t N, int32_t r,
                               qlora_stream_t stream);
 
 /*
+ * 8-bit activation checkpoints (page "SFT（四）：QLoRA的4-bit量化与LoRA微调原理",
+ * §26.2 为什么开启 Gradient Checkpointing: what a layer keeps between its forward
+ * and its backward costs memory; here the kept matrix costs 1.0625 bytes an
+ * element instead of 2).  A bf16 matrix rows x cols (cols % 64 == 0) is cut
+ * into blocks of 64 along each row:
+ *   scale = fl32(amax / 127), or 1 where that is below 2^-126 (an all-zero
+ *           block among them);
+ *   code  = rint(fl32(x / scale)), ties to even: -127 .. 127;
+ *   value = RN_bf16(fl32(code · scale)): within scale / 2 and one bf16 rounding of x.
+ *   codes  : rows x cols int8, row-major.     scales : rows x (cols / 64) fp32.
+ * Device errors of the quantizer: NONFINITE (a NaN or infinity; that block's
+ * codes are then unspecified).  Host errors: INVALID_ARG, UNSUPPORTED
+ * (cols % 64 != 0, more than 2^38 elements), CUDA.  X may not overlap the codes
+ * or the scales.
+ */
+typedef struct qlora_act8 {
+  int64_t rows, cols;
+  int8_t* codes;    /* device, 16-byte aligned */
+  float*  scales;   /* device, 16-byte aligned */
+} qlora_act8;
+qlora_status qlora_act8_quantize(const uint16_t* X, const qlora_act8* out, int32_t* d_status,
+                                 qlora_stream_t stream);
+qlora_status qlora_act8_dequantize(const qlora_act8* in, uint16_t* X, qlora_stream_t stream);
+
+/*
+ * qlora_linear_bwd for a layer whose input was kept as an 8-bit checkpoint
+ * (M x K): dX and dB do not see X, and dA = X̂ᵀ·dZ reads the codes straight into
+ * the tensor-core operand; X̂ is never written to memory.  Zc (the forward's) is
+ * needed: a Zc recomputed from X̂ would not be the one the forward used.
+ * grad_dtype is the type of dA and dB: QLORA_DTYPE_F32, or QLORA_DTYPE_BF16
+ * for adapters whose gradients are kept in their own type (the operands carry
+ * 8 bits either way: dZ and Zc are bf16).  X may be NULL when X8 is not and the
+ * other way round: with X this is qlora_linear_bwd with a choice of grad_dtype.
+ * Same shapes, workspace (qlora_linear_bwd_workspace_size) and streams as there.
+ */
+qlora_status qlora_linear_bwd_act8(int64_t M, int64_t K, int64_t N, int32_t r,
+                                   const uint16_t* dY, const uint16_t* X, const qlora_act8* X8,
+                                   const uint16_t* Zc, const qlora_nf4_state* W, const uint16_t* A,
+                                   const uint16_t* B, float c, uint16_t* dX, void* dA, void* dB,
+                                   qlora_dtype grad_dtype, void* ws, size_t ws_bytes,
+                                   int32_t* d_status, qlora_stream_t stream);
+
+/*
+ * Gated feed-forward block over two frozen-base layers of the same input (the
+ * gate and up projections of a decoder layer; page "QLoRA：冻结的 4-bit 权重怎样
+ * 参与一次微调", §量化基座与可训练支路怎样相加, twice):
+ *
+ *   g = X·Ŵg + c·(X·Ag)·Bg,   u = X·Ŵu + c·(X·Au)·Bu,   H = RN_bf16(act(g) · u)
+ *
+ * g and u stay in fp32 between the products and H.  act: QLORA_ACT_SILU
+ * (g·sigmoid(g)) or QLORA_ACT_GELU (the tanh form).
+ *   X : bf16 M×K   Wg, Wu : NF4 (or INT4) states of K×N, each with its own scales
+ *   Ag, Au : bf16 K×r   Bg, Bu : bf16 r×N   H : bf16 M×N output
+ *   saved : what the backward needs, or NULL (inference).  Zg and Zu (bf16 M×r,
+ *           bf16(c·X·A)) and either G and U (g and u rounded to bf16, M×N) or,
+ *           with G and U null, G8/G_scales and U8/U_scales: the 8-bit
+ *           checkpoints of those bf16 matrices, the same bits that
+ *           qlora_act8_quantize would give (NONFINITE likewise).
+ * Shapes: M >= 1, K % 64 == 0, N % 64 == 0, 1 <= r <= 64, else UNSUPPORTED.
+ * Outputs may not overlap each other or the inputs.  ws: at least
+ * qlora_gated_fwd_workspace_size bytes, for this call alone until it has run.
+ */
+typedef struct qlora_gated_saved {
+  uint16_t *G, *U;
+  int8_t *G8, *U8;
+  float *G_scales, *U_scales;
+  uint16_t *Zg, *Zu;
+} qlora_gated_saved;
+size_t qlora_gated_fwd_workspace_size(int64_t M, int64_t K, int64_t N, int32_t r);
+qlora_status qlora_gated_fwd(int64_t M, int64_t K, int64_t N, int32_t r, const uint16_t* X,
+                             const qlora_nf4_state* Wg, const qlora_nf4_state* Wu,
+                             const uint16_t* Ag, const uint16_t* Bg, const uint16_t* Au,
+                             const uint16_t* Bu, float c, qlora_act act, uint16_t* H,
+                             const qlora_gated_saved* saved, void* ws, size_t ws_bytes,
+                             int32_t* d_status, qlora_stream_t stream);
+
+/*
+ * Its backward (same page, §冻结权重为什么仍然需要输入梯度, through the product):
+ *   dG = bf16(dH·u·act'(g)),  dU = bf16(dH·act(g)),  dZ = bf16(c·d·Bᵀ),
+ *   dX = dG·Ŵgᵀ + dU·Ŵuᵀ + dZg·Agᵀ + dZu·Auᵀ,  dA = Xᵀ·dZ,  dB = Zᵀ·d
+ * with g and u as `saved` keeps them (8-bit ones by their values).  No gradient
+ * for the frozen weights.  X, or with X null its 8-bit checkpoint X8; dAg, dAu
+ * K×r and dBg, dBu r×N of grad_dtype; dX bf16 M×K.  Streams as
+ * qlora_linear_bwd.  ws: at least qlora_gated_bwd_workspace_size bytes (dG and
+ * dU, 4·M·N bytes, are the most of it).
+ */
+size_t qlora_gated_bwd_workspace_size(int64_t M, int64_t K, int64_t N, int32_t r);
+qlora_status qlora_gated_bwd(int64_t M, int64_t K, int64_t N, int32_t r, const uint16_t* dH,
+                             const uint16_t* X, const qlora_act8* X8,
+                             const qlora_gated_saved* saved, const qlora_nf4_state* Wg,
+                             const qlora_nf4_state* Wu, const uint16_t* Ag, const uint16_t* Bg,
+                             const uint16_t* Au, const uint16_t* Bu, float c, qlora_act act,
+                             uint16_t* dX, void* dAg, void* dBg, void* dAu, void* dBu,
+                             qlora_dtype grad_dtype, void* ws, size_t ws_bytes, int32_t* d_status,
+                             qlora_stream_t stream);
+
+/*
+ * Softmax cross entropy behind a frozen head, in pieces of the vocabulary (no
+ * counterpart on the pages beyond the training step they describe: the loss
+ * that the layer's output gradient comes from).  The logits l = X·Ŵ never
+ * reach memory:
+ *   lse_i = log Σ_{v < vocab} exp(l_iv),   loss_i = lse_i - l_i[labels_i]
+ *   dX_i  = dloss_i · (Σ_v softmax(l_i)_v Ŵ_v - Ŵ_{labels_i})
+ *   X : bf16 M×K    W : state of the K×N head (K % 64 == N % 64 == 0)
+ *   vocab : 1 .. N; the head's columns from vocab on are padding
+ *   labels : int64 M.  A row whose label is ignore_index has loss 0 and dX 0.
+ *            Any other label outside 0 .. vocab-1 is the device error
+ *            INVALID_ARG, and the row is treated the same way.
+ *   loss, lse, dloss : fp32 M     dX : bf16 M×K
+ * The logits are fp32 sums of bf16 products; the sums of exponentials, loss
+ * and lse are fp32.  The backward forms the logits of a piece again, rounds
+ * dloss·(softmax - onehot) to bf16 and adds the pieces' products in fp32.
+ */
+size_t qlora_head_loss_fwd_workspace_size(int64_t M, int64_t K, int64_t N);
+qlora_status qlora_head_loss_fwd(int64_t M, int64_t K, int64_t N, int64_t vocab, const uint16_t* X,
+                                 const qlora_nf4_state* W, const int64_t* labels,
+                                 int64_t ignore_index, float* loss, float* lse, void* ws,
+                                 size_t ws_bytes, int32_t* d_status, qlora_stream_t stream);
+size_t qlora_head_loss_bwd_workspace_size(int64_t M, int64_t K, int64_t N);
+qlora_status qlora_head_loss_bwd(int64_t M, int64_t K, int64_t N, int64_t vocab,
+                                 const float* dloss, const uint16_t* X, const float* lse,
+                                 const qlora_nf4_state* W, const int64_t* labels,
+                                 int64_t ignore_index, uint16_t* dX, void* ws, size_t ws_bytes,
+                                 int32_t* d_status, qlora_stream_t stream);
+
+/*
  * Merge / export — page "QLoRA：冻结的 4-bit 权重怎样参与一次微调",
  * §Merge 后还是不是训练时的函数: after training, the layer's function is Ŵ
  * together with the adapter; one delivery is the dense merged weight
@@ -367,6 +499,9 @@ qlora_status qlora_selftest_bounded_wait(int64_t limit_ns, int32_t* d_status, ql
 #define QLORA_PROF_DEQUANTIZE 4   /* standalone dequantization           */
 #define QLORA_PROF_GEMV       5   /* M <= 16 GEMV                        */
 #define QLORA_PROF_OTHER      6   /* GEMV split sums                     */
+#define QLORA_PROF_ACT8       7   /* 8-bit activation codec              */
+#define QLORA_PROF_GATED      8   /* gated block (all but its rank-r products) */
+#define QLORA_PROF_LOSS       9   /* head loss                           */
 qlora_status qlora_profile_enable(int32_t on);
 qlora_status qlora_profile_read(int32_t kind, double* total_ms, int64_t* launches);
 qlora_status qlora_profile_reset(void);
