@@ -383,7 +383,7 @@ def _linear_backward_act8(dY, X, Zc, w, A, B, c, dX, dA, dB, status, workspace, 
     _args.tensor(B, "B", (r, N), dev)
     if Zc is not None:
         _args.tensor(Zc, "Zc", (M, r), dev)
-    with torch.cuda.device(dev):
+    with _args.on(dev):
         out = []
         for t, name, shape, dt in ((dX, "dX", (M, K), torch.bfloat16), (dA, "dA", (K, r), grad_dtype),
                                    (dB, "dB", (r, N), grad_dtype)):
@@ -399,6 +399,6 @@ def _linear_backward_act8(dY, X, Zc, w, A, B, c, dX, dA, dB, status, workspace, 
                                         C.byref(X.cstruct()) if is8 else None, _args.ptr(Zc),
                                         C.byref(w.cstruct()), A.data_ptr(), B.data_ptr(), float(c),
                                         *(t.data_ptr() for t in out), gcode, ws.data_ptr(), ws.numel(),
-                                        status.data_ptr(), _stream()), "qlora_linear_bwd_act8")
+                                        status.data_ptr(), _args.stream(dev)), "qlora_linear_bwd_act8")
         _finish(status, own, "qlora_linear_bwd_act8")
     return tuple(out)

@@ -8,13 +8,32 @@ kernel.
 """
 from __future__ import annotations
 
-import ctypes as C
+import contextlib
 
 import torch
 
 from ._lib import QLORA_DTYPE_BF16, QLORA_DTYPE_F32
 
 GRAD_DTYPES = {torch.float32: QLORA_DTYPE_F32, torch.bfloat16: QLORA_DTYPE_BF16}
+
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_here = contextlib.nullcontext()
+
+
+def on(dev):
+    """A context in which dev (a CUDA device with an index) is current; the
+    usual case, that it is already, costs no switch."""
+    if _current_device is not None and _current_device() == dev.index:
+        return _here
+    return torch.cuda.device(dev)
+
+
+def stream(dev):
+    """The raw current stream of dev."""
+    if _raw_stream is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def cuda_2d(t, name):
@@ -38,17 +57,22 @@ def weight(w, name, shape, dev):
     """An NF4Weight of `shape` whose buffers hold what its struct promises."""
     if tuple(w.shape) != shape:
         raise ValueError(f"{name} must be {shape[0]} x {shape[1]}, not {tuple(w.shape)}")
-    n1 = (shape[0] * shape[1] + 63) // 64
+    numel = shape[0] * shape[1]
+    n1 = (numel + 63) // 64
+    _buffer(w.packed, torch.uint8, (numel + 1) // 2, name, dev)
     if w.double_quant:
-        need = ((w.packed, torch.uint8, (shape[0] * shape[1] + 1) // 2), (w.code8, torch.uint8, n1),
-                (w.s2, torch.float32, (n1 + 255) // 256), (w.offset, torch.float32, 1))
+        _buffer(w.code8, torch.uint8, n1, name, dev)
+        _buffer(w.s2, torch.float32, (n1 + 255) // 256, name, dev)
+        _buffer(w.offset, torch.float32, 1, name, dev)
     else:
-        need = ((w.packed, torch.uint8, (shape[0] * shape[1] + 1) // 2), (w.absmax, torch.float32, n1))
-    for t, dtype, n in need:
-        if t is None or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-            raise TypeError(f"{name}: a buffer is missing, or not a contiguous {dtype} tensor on {dev}")
-        if t.numel() != n:
-            raise ValueError(f"{name}: a buffer has {t.numel()} elements, not {n}")
+        _buffer(w.absmax, torch.float32, n1, name, dev)
+
+
+def _buffer(t, dtype, n, name, dev):
+    if t is None or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise TypeError(f"{name}: a buffer is missing, or not a contiguous {dtype} tensor on {dev}")
+    if t.numel() != n:
+        raise ValueError(f"{name}: a buffer has {t.numel()} elements, not {n}")
 
 
 def grad_code(dtype):
@@ -59,10 +83,6 @@ def grad_code(dtype):
 
 def ptr(t):
     return None if t is None else t.data_ptr()
-
-
-def stream():
-    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
 def workspace(given, nbytes, dev):

@@ -56,7 +56,7 @@ def act8_quantize(X: torch.Tensor, *, out: Act8 | None = None, status: torch.Ten
     is a multiple of 64.  A NaN or infinity in X is a device error."""
     from . import _finish, new_status
     M, K, dev = _args.cuda_2d(X, "X")
-    with torch.cuda.device(dev):
+    with _args.on(dev):
         if out is None:
             out = Act8.empty(M, K, dev)
         else:
@@ -64,7 +64,7 @@ def act8_quantize(X: torch.Tensor, *, out: Act8 | None = None, status: torch.Ten
         own = status is None
         status = new_status(dev) if own else status
         st = out.cstruct()
-        check(lib.qlora_act8_quantize(X.data_ptr(), C.byref(st), status.data_ptr(), _args.stream()),
+        check(lib.qlora_act8_quantize(X.data_ptr(), C.byref(st), status.data_ptr(), _args.stream(dev)),
               "qlora_act8_quantize")
         _finish(status, own, "qlora_act8_quantize")
     return out
@@ -76,11 +76,11 @@ def act8_dequantize(a: Act8, *, out: torch.Tensor | None = None) -> torch.Tensor
         raise TypeError("a must be an Act8 on a CUDA device")
     dev = a.device
     check_act8(a, "a", tuple(a.codes.shape), dev)
-    with torch.cuda.device(dev):
+    with _args.on(dev):
         if out is None:
             out = torch.empty(a.codes.shape, dtype=torch.bfloat16, device=dev)
         else:
             _args.tensor(out, "out", a.codes.shape, dev)
         st = a.cstruct()
-        check(lib.qlora_act8_dequantize(C.byref(st), out.data_ptr(), _args.stream()), "qlora_act8_dequantize")
+        check(lib.qlora_act8_dequantize(C.byref(st), out.data_ptr(), _args.stream(dev)), "qlora_act8_dequantize")
     return out

@@ -180,34 +180,58 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return d;
 }
 
+template <uint32_t kSel>
+__device__ __forceinline__ uint32_t prmt_c(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "n"(kSel));
+  return d;
+}
+
 // 8 packed nibbles (4 bytes, first weight in the high nibble of byte 0) ->
 // 8 bf16 from the per-block table whose high and low bytes are split into
-// H[0..3] and L[0..3] (entry j's byte in byte j%4 of H[j/4] / L[j/4]).
+// H[0..3] and L[0..3] (entry j's byte in byte j%4 of H[j/4] / L[j/4]).  The
+// byte permutes and logic share one pipe at half the issue rate, and its 21
+// operations per 8 weights are what decoding costs.
 __device__ __forceinline__ uint4 decode8(uint32_t p, const uint32_t (&H)[4],
                                          const uint32_t (&L)[4]) {
   // selector nibbles: low 3 bits pick a byte within a plane pair, bit 3
   // (moved to the "+4" position) picks the pair
   const uint32_t s = p & 0x77777777u;
-  const uint32_t b = ((p >> 1) & 0x44444444u) | 0x32103210u;
+  uint32_t b;
+  // ((p >> 1) & 0x44444444) | 0x32103210 in one operation after the shift
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(b) : "r"(p >> 1), "r"(0x44444444u), "r"(0x32103210u));
   uint4 o;
   {
     const uint32_t hF = prmt(prmt(H[0], H[1], s), prmt(H[2], H[3], s), b);
     const uint32_t lF = prmt(prmt(L[0], L[1], s), prmt(L[2], L[3], s), b);
-    o.x = prmt(lF, hF, 0x4051u);
-    o.y = prmt(lF, hF, 0x6273u);
+    o.x = prmt_c<0x4051u>(lF, hF);
+    o.y = prmt_c<0x6273u>(lF, hF);
   }
   {
     const uint32_t s2 = s >> 16, b2 = b >> 16;
     const uint32_t hF = prmt(prmt(H[0], H[1], s2), prmt(H[2], H[3], s2), b2);
     const uint32_t lF = prmt(prmt(L[0], L[1], s2), prmt(L[2], L[3], s2), b2);
-    o.z = prmt(lF, hF, 0x4051u);
-    o.w = prmt(lF, hF, 0x6273u);
+    o.z = prmt_c<0x4051u>(lF, hF);
+    o.w = prmt_c<0x6273u>(lF, hF);
   }
   return o;
 }
 
 // Per-block table: entry j = bf16(C_j * a) (fp32 product, then bf16).
 __device__ __forceinline__ void build_lut(const float* C, float a, uint32_t (&H)[4], uint32_t (&L)[4]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(C[2 * i] * a, C[2 * i + 1] * a);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    H[q] = prmt(w[2 * q], w[2 * q + 1], 0x7531u);
+    L[q] = prmt(w[2 * q], w[2 * q + 1], 0x6420u);
+  }
+}
+
+// The same for the NF4 codebook, its values immediates of the products.
+__device__ __forceinline__ void build_lut_nf4(float a, uint32_t (&H)[4], uint32_t (&L)[4]) {
+  constexpr float C[16] = {QNF4_TABLE_VALUES};
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(C[2 * i] * a, C[2 * i + 1] * a);
@@ -288,9 +312,8 @@ __device__ __forceinline__ RowFetch fetch_row(const typename ModeTypes<kMode>::A
   if (sv->code8 == nullptr) {
     asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(f.absv) : "l"(sv->absmax + blk));
   } else {
-    uint16_t qv;
-    asm volatile("ld.global.nc.u8 %0, [%1];" : "=h"(qv) : "l"(sv->code8 + blk));
-    f.q = qv;
+    // into a 32-bit register: a widening of a 16-bit one would wait for the load here
+    asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(f.q) : "l"(sv->code8 + blk));
     asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(f.s2v) : "l"(sv->s2 + (blk >> 8)));
   }
   return f;
@@ -707,19 +730,28 @@ __global__ void __launch_bounds__(kFThreads, 1)
           if (*abort_flag || !mbar_wait(&full_b[sb], phb)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a0 = smem_u32(sA + sa * kFA), b0 = smem_u32(sB + sb * kFB);
-          const uint32_t acc = kk > 0 ? 1u : 0u;
+          if (kk == 0) {
+            // first K-step of a tile: each accumulator as soon as it is drained
 #pragma unroll
-          for (int h = 0; h < kFSlices; ++h) {
-            if (kk == 0) {   // first K-step of a tile: wait until this accumulator is drained
+            for (int h = 0; h < kFSlices; ++h) {
               if (*abort_flag || !mbar_wait(&tempty[h], tph)) { ok = false; break; }
               tc_fence_after();
-            }
-            if (kLayer || h < nh) {
+              if (kLayer || h < nh) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) mma(h, a0, b0, j, (acc || j > 0) ? 1u : 0u);
+                for (int j = 0; j < 4; ++j) mma(h, a0, b0, j, j > 0 ? 1u : 0u);
+              }
             }
+            if (!ok) break;
+          } else {
+            // the two accumulators in turn: a product waits for the one before
+            // it on the same accumulator (171 clocks from one to the next at N =
+            // 256, 128 where two alternate)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int h = 0; h < kFSlices; ++h)
+                if (kLayer || h < nh) mma(h, a0, b0, j, 1u);
           }
-          if (!ok) break;
           umma_commit_pair_mc(&empty_a[sa], 0x3);
           umma_commit_pair_mc(&empty_b[sb], 0x3);
         }
@@ -770,8 +802,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
         ok = false;
         return;
       }
-      uint8_t* brow = sB + s * kFB + R * 128;
-      const uint32_t sw = static_cast<uint32_t>(R & 7);
+      // row R of the stage, its 16-byte chunk bits holding the swizzle
+      const uint32_t brow = smem_u32(sB) + s * kFB + R * 128 + ((R & 7) << 4);
       if (f.valid) {
         const ScaleView* sv = sv1;
         float off = off1;
@@ -785,14 +817,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
         build_lut(kNF4g + 16 * sv->codebook, a, H, L);
         const uint32_t pw[8] = {f.p0.x, f.p0.y, f.p0.z, f.p0.w, f.p1.x, f.p1.y, f.p1.z, f.p1.w};
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(brow + ((static_cast<uint32_t>(c) ^ sw) << 4)) =
-              decode8(pw[c], H, L);
+        for (uint32_t c = 0; c < 8; ++c) sts128(brow ^ (c << 4), decode8(pw[c], H, L));
       } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(brow + ((static_cast<uint32_t>(c) ^ sw) << 4)) =
-              make_uint4(0, 0, 0, 0);
+        for (uint32_t c = 0; c < 8; ++c) sts128(brow ^ (c << 4), make_uint4(0, 0, 0, 0));
       }
       // the rows are visible to the tensor core (async proxy), then CTA 0's
       // barrier of the stage counts this warp

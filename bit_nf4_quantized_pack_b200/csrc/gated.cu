@@ -98,7 +98,7 @@ int tiles_of(int64_t n, int per) { return static_cast<int>((n + per - 1) / per);
 }  // namespace
 
 size_t gated_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r) {
-  (void)N;
+  if (gated_rows_fit(M, K, N)) return gated_rows_workspace_bytes(M, K, N, r);
   const int rp = padded_rank(r);
   // Zg and Zu (a copy padded to rp columns where the caller keeps them with r),
   // and both A padded to rp columns when r is not a multiple of 8
@@ -118,6 +118,7 @@ cudaError_t launch_gated_fwd(int64_t M, int64_t K, int64_t N, int r, const uint1
                              const GatedWeights& w, uint16_t* H, const GatedKept& kept, void* ws,
                              size_t ws_bytes, int32_t* d_status, cudaStream_t st, int num_sms) {
   (void)num_sms;
+  if (gated_rows_fit(M, K, N)) return launch_gated_rows(M, K, N, r, X, w, H, kept, ws, ws_bytes, d_status, st);
   WsCursor cur{static_cast<char*>(ws), ws_bytes};
   const int rp = padded_rank(r);
   const bool pad = rp != r;
@@ -130,8 +131,7 @@ cudaError_t launch_gated_fwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   cudaError_t e = cudaSuccess;
   const uint16_t *Ag = w.Ag, *Au = w.Au;
   if (pad) {
-    e = launch_pad(w.Ag, K, r, Apg, rp, st);
-    if (e == cudaSuccess) e = launch_pad(w.Au, K, r, Apu, rp, st);
+    e = launch_pad_sets(PadSet{{w.Ag, w.Au}, {Apg, Apu}, {K, K}}, 2, r, rp, st);
     if (e != cudaSuccess) return e;
     Ag = Apg;
     Au = Apu;
@@ -216,10 +216,7 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   cudaError_t e = cudaSuccess;
   const uint16_t *Ag = w.Ag, *Au = w.Au, *Zg = kept.Zg, *Zu = kept.Zu;
   if (pad) {
-    e = launch_pad(w.Ag, K, r, Apg, rp, st);
-    if (e == cudaSuccess) e = launch_pad(w.Au, K, r, Apu, rp, st);
-    if (e == cudaSuccess) e = launch_pad(kept.Zg, M, r, Zpg, rp, st);
-    if (e == cudaSuccess) e = launch_pad(kept.Zu, M, r, Zpu, rp, st);
+    e = launch_pad_sets(PadSet{{w.Ag, w.Au, kept.Zg, kept.Zu}, {Apg, Apu, Zpg, Zpu}, {K, K, M, M}}, 4, r, rp, st);
     if (e != cudaSuccess) return e;
     Ag = Apg;
     Au = Apu;

@@ -218,6 +218,13 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
                              void* dBg, void* dAu, void* dBu, bool grad_bf16, void* ws,
                              size_t ws_bytes, int32_t* d_status, cudaStream_t st, int num_sms);
 
+// gated_rows.cu — the gated forward for few rows (see there)
+bool gated_rows_fit(int64_t M, int64_t K, int64_t N);
+size_t gated_rows_workspace_bytes(int64_t M, int64_t K, int64_t N, int r);
+cudaError_t launch_gated_rows(int64_t M, int64_t K, int64_t N, int r, const uint16_t* X,
+                              const GatedWeights& w, uint16_t* H, const GatedKept& kept, void* ws,
+                              size_t ws_bytes, int32_t* d_status, cudaStream_t st);
+
 // loss.cu — softmax cross entropy behind an NF4 head
 size_t loss_fwd_workspace_bytes(int64_t M, int64_t N);
 size_t loss_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N);

@@ -691,5 +691,39 @@ cudaError_t launch_pad(const uint16_t* src, int64_t rows, int r, uint16_t* dst, 
   return cudaGetLastError();
 }
 
+// The same for several matrices of one rank in one launch (blockIdx.y).
+struct PadSet {
+  const uint16_t* src[4];
+  uint16_t* dst[4];
+  int64_t rows[4];
+};
+
+__global__ void __launch_bounds__(256) pad_sets_kernel(PadSet p, int r, int rp) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int m = blockIdx.y;
+  const int64_t total = p.rows[m] * rp;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t row = i / rp;
+    const int col = static_cast<int>(i - row * rp);
+    p.dst[m][i] = col < r ? p.src[m][row * r + col] : static_cast<uint16_t>(0);
+  }
+}
+
+inline cudaError_t launch_pad_sets(const PadSet& p, int n, int r, int rp, cudaStream_t st) {
+  int64_t most = 1;
+  for (int i = 0; i < n; ++i) most = p.rows[i] > most ? p.rows[i] : most;
+  const int64_t want = (most * rp + 255) / 256;
+  const unsigned grid = static_cast<unsigned>(want < 296 ? want : 296);
+  cudaError_t e;
+  {
+    ProfScope prof(kProfOther, st);
+    e = launch_pdl(pad_sets_kernel, dim3(grid, static_cast<unsigned>(n)), dim3(256), 0, st, 1, p, r, rp);
+  }
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
 }  // namespace
 }  // namespace qnf4

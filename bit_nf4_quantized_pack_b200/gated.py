@@ -92,7 +92,7 @@ def gated_forward(X, wg, wu, Ag, Bg, Au, Bu, c: float, *, act: str = "silu", sav
     M, K, dev = _args.cuda_2d(X, "X")
     code = _act_code(act)
     N, r = _weights(K, dev, wg, wu, Ag, Bg, Au, Bu)
-    with torch.cuda.device(dev):
+    with _args.on(dev):
         if H is None:
             H = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
         else:
@@ -107,7 +107,7 @@ def gated_forward(X, wg, wu, Ag, Bg, Au, Bu, c: float, *, act: str = "silu", sav
         check(lib.qlora_gated_fwd(M, K, N, r, X.data_ptr(), C.byref(wg.cstruct()), C.byref(wu.cstruct()),
                                   Ag.data_ptr(), Bg.data_ptr(), Au.data_ptr(), Bu.data_ptr(), float(c), code,
                                   H.data_ptr(), kept, ws.data_ptr(), ws.numel(), status.data_ptr(),
-                                  _args.stream()), "qlora_gated_fwd")
+                                  _args.stream(dev)), "qlora_gated_fwd")
         _finish(status, own, "qlora_gated_fwd")
     return H, saved
 
@@ -131,7 +131,7 @@ def gated_backward(dH, X, saved: GatedSaved, wg, wu, Ag, Bg, Au, Bu, c: float, *
         raise ValueError(f"dH must have {Nw} columns, not {N}")
     if not isinstance(saved, GatedSaved):
         raise TypeError("saved must be the GatedSaved of the forward")
-    with torch.cuda.device(dev):
+    with _args.on(dev):
         kept = saved.cstruct(M, N, r, dev)
         out = []
         for t, name, shape, dt in ((dX, "dX", (M, K), torch.bfloat16), (dAg, "dAg", (K, r), grad_dtype),
@@ -151,6 +151,6 @@ def gated_backward(dH, X, saved: GatedSaved, wg, wu, Ag, Bg, Au, Bu, c: float, *
                                   C.byref(kept), C.byref(wg.cstruct()), C.byref(wu.cstruct()),
                                   Ag.data_ptr(), Bg.data_ptr(), Au.data_ptr(), Bu.data_ptr(), float(c), code,
                                   *(t.data_ptr() for t in out), gcode, ws.data_ptr(), ws.numel(),
-                                  status.data_ptr(), _args.stream()), "qlora_gated_bwd")
+                                  status.data_ptr(), _args.stream(dev)), "qlora_gated_bwd")
         _finish(status, own, "qlora_gated_bwd")
     return tuple(out)

@@ -36,7 +36,7 @@ def head_loss_forward(X, w, labels, *, vocab: int | None = None, ignore_index: i
     0; any other label outside 0 .. vocab - 1 is a device error."""
     from . import _finish, new_status
     M, K, N, vocab, dev = _head(X, w, labels, vocab)
-    with torch.cuda.device(dev):
+    with _args.on(dev):
         out = []
         for t, name in ((loss, "loss"), (lse, "lse")):
             if t is None:
@@ -50,7 +50,7 @@ def head_loss_forward(X, w, labels, *, vocab: int | None = None, ignore_index: i
         status = new_status(dev) if own else status
         check(lib.qlora_head_loss_fwd(M, K, N, vocab, X.data_ptr(), C.byref(w.cstruct()), labels.data_ptr(),
                                       int(ignore_index), out[0].data_ptr(), out[1].data_ptr(), ws.data_ptr(),
-                                      ws.numel(), status.data_ptr(), _args.stream()), "qlora_head_loss_fwd")
+                                      ws.numel(), status.data_ptr(), _args.stream(dev)), "qlora_head_loss_fwd")
         _finish(status, own, "qlora_head_loss_fwd")
     return tuple(out)
 
@@ -63,7 +63,7 @@ def head_loss_backward(dloss, X, lse, w, labels, *, vocab: int | None = None, ig
     M, K, N, vocab, dev = _head(X, w, labels, vocab)
     _args.tensor(dloss, "dloss", (M,), dev, torch.float32)
     _args.tensor(lse, "lse", (M,), dev, torch.float32)
-    with torch.cuda.device(dev):
+    with _args.on(dev):
         if dX is None:
             dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
         else:
@@ -75,6 +75,6 @@ def head_loss_backward(dloss, X, lse, w, labels, *, vocab: int | None = None, ig
         check(lib.qlora_head_loss_bwd(M, K, N, vocab, dloss.data_ptr(), X.data_ptr(), lse.data_ptr(),
                                       C.byref(w.cstruct()), labels.data_ptr(), int(ignore_index),
                                       dX.data_ptr(), ws.data_ptr(), ws.numel(), status.data_ptr(),
-                                      _args.stream()), "qlora_head_loss_bwd")
+                                      _args.stream(dev)), "qlora_head_loss_bwd")
         _finish(status, own, "qlora_head_loss_bwd")
     return dX

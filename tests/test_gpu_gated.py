@@ -173,3 +173,34 @@ def test_outputs_stay_inside_and_repeat():
         H2, kept2 = q.gated_forward(case.t["X"], *case.args, save="int8")
         again = q.gated_backward(case.t["dH"], case.t["X"], kept2, *case.args, grad_dtype=torch.bfloat16)
         assert torch.equal(H, H2) and all(torch.equal(a, b) for a, b in zip(again, out.values()))
+
+
+@pytest.mark.parametrize("M,K,N,r,dq", [(1, 4096, 11008, 16, True), (16, 2048, 22016, 64, False),
+                                        (128, 4096, 4160, 8, True), (70, 1088, 11008, 24, True),
+                                        (200, 4096, 11008, 16, True)])
+def test_forward_at_full_width(M, K, N, r, dq):
+    """Long runs of units per SM, against fp64 products of the dequantized
+    weights on the device: the bound of the small cases, the decode's own
+    double rounding (one bf16 step of one weight in 2^16) aside, which Frobenius
+    norms do not see."""
+    q = _q()
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+
+    def t(*shape, sigma):
+        return (torch.randn(*shape, generator=g, device="cuda") * sigma).to(torch.bfloat16)
+    X, c = t(M, K, sigma=1.0), 2.0
+    W = [q.quantize(t(K, N, sigma=0.02), double_quant=dq) for _ in range(2)]
+    A, B = [t(K, r, sigma=0.02) for _ in range(2)], [t(r, N, sigma=0.02) for _ in range(2)]
+    pre = []
+    for i in range(2):
+        Z = (c * (X.double() @ A[i].double()))
+        pre.append(X.double() @ q.dequantize(W[i]).double() + Z @ B[i].double())
+    want = pre[0] * torch.sigmoid(pre[0]) * pre[1]
+    for _ in range(3):
+        H, saved = q.gated_forward(X, W[0], W[1], A[0], B[0], A[1], B[1], c, save="bf16")
+        for got, ref in ((H, want), (saved.G, pre[0]), (saved.U, pre[1])):
+            rel = ((got.double() - ref).norm() / ref.norm()).item()
+            # one rounding to bf16: 2^-8 / sqrt(3) at most in this norm, and Z's
+            # on the small adapter term
+            assert rel <= 2.0 ** -8, rel
+            assert ((got.double() - ref).abs().max() / ref.abs().max()).item() <= 2.0 ** -7
