@@ -551,7 +551,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (through a shuffle, so that the compiler knows it to be the same for the warp)
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   // the pair is the cluster (2 x 1 x 1): rank 0 issues the MMAs
   const int rank = static_cast<int>(blockIdx.x & 1);
   const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
@@ -696,83 +697,100 @@ __global__ void __launch_bounds__(kFThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------- MMA issuer (CTA 0 only) ----------------------
-    if (lane == 0 && rank == 0) {
+    // The whole warp runs the loop and its elected lane issues: every
+    // instruction of this warp waits for the decoders of its scheduler, so the
+    // products' operands are kept to one addition each (descriptors differ from
+    // the first stage's in their low word only).
+    if (rank == 0) {
       // forward: D[m][n] += act[m][k] * Ŵtile[k][n] (tile MN-major, as B);
       // backward: D[n][m] += Ŵtile[n][k] * dY[m][k] (tile K-major, as A)
       constexpr uint32_t idesc = kBwd ? idesc_bf16_f32(256, kFAccCols, 0, 0)
                                       : idesc_bf16_f32(256, kFAccCols, 0, 1);
-      uint32_t ia = 0, ib = 0, tc = 0;
+      // activation operand: slices 16 KB apart, 16-wide K slices 32 bytes apart;
+      // weight operand: K slices 32 bytes (K-major) or 2 KB (MN-major) apart
+      const uint64_t act0 = smem_desc(smem_u32(sA), 16, 1024);
+      const uint64_t wgt0 = kBwd ? smem_desc(smem_u32(sB), 16, 1024) : smem_desc(smem_u32(sB), 8192, 1024);
+      // the weight operand of a LoRA step lies in an activation stage
+      const uint64_t lor0 = kBwd ? act0 : smem_desc(smem_u32(sA), 8192, 1024);
+      constexpr uint32_t kWSlice = kBwd ? 2 : 128;
+      const uint32_t acthi = static_cast<uint32_t>(act0 >> 32), wgthi = static_cast<uint32_t>(wgt0 >> 32);
+      const uint32_t elected = elect_one();
+      uint32_t sa = 0, pha = 0, sb = 0, phb = 0, tc = 0;
       bool ok = true;
-      auto wait_a = [&](uint32_t& s) -> bool {
-        s = ia % kFAStages;
-        const uint32_t ph = (ia / kFAStages) & 1;
-        ++ia;
-        return !*abort_flag && mbar_wait(&full_a[s], ph);
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return mbar_try_wait(bar, parity) || (!*abort_flag && mbar_wait(bar, parity));
       };
-      // one 16-wide K slice j of accumulator h: `w0` the weight operand
-      // (decoded tile, or B / A in the LoRA step), `a0` the activation stage
-      auto mma = [&](int h, uint32_t a0, uint32_t w0, int j, uint32_t accum) {
-        const uint64_t adesc = smem_desc(a0 + h * 16384 + j * 32, 16, 1024);
+      auto next_a = [&]() {
+        if (++sa == kFAStages) { sa = 0; pha ^= 1; }
+      };
+      // one 16-wide K slice of accumulator h: `al` the activation slice, `wl`
+      // the weight slice (low words)
+      auto mma = [&](int h, uint32_t al, uint32_t wl, uint32_t accum) {
         if (kBwd)
-          umma_bf16_pair(tmem + h * kFAccCols, smem_desc(w0 + j * 32, 16, 1024), adesc, idesc, accum);
+          umma_bf16_pair_lo(elected, tmem + h * kFAccCols, wl, wgthi, al + h * 1024, acthi, idesc, accum);
         else
-          umma_bf16_pair(tmem + h * kFAccCols, adesc, smem_desc(w0 + j * 2048, 8192, 1024), idesc,
-                         accum);
+          umma_bf16_pair_lo(elected, tmem + h * kFAccCols, al + h * 1024, acthi, wl, wgthi, idesc, accum);
       };
       for (int tile = pair; tile < num_tiles && ok; tile += npairs, ++tc) {
         const uint32_t tph = (tc & 1) ^ 1;       // parity of the previous tile's release
         const int nh = tile_slices<kMode>(args.M, (tile % args.m_tiles) * kFPairRows);
         for (int kk = 0; kk < args.nk; ++kk) {
-          uint32_t sa;
-          if (!wait_a(sa)) { ok = false; break; }
-          const uint32_t sb = ib % kFBStages, phb = (ib / kFBStages) & 1;
-          ++ib;
-          if (*abort_flag || !mbar_wait(&full_b[sb], phb)) { ok = false; break; }
+          if (!wait(&full_a[sa], pha) || !wait(&full_b[sb], phb)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + sa * kFA), b0 = smem_u32(sB + sb * kFB);
+          const uint32_t al = static_cast<uint32_t>(act0) + sa * (kFA >> 4);
+          const uint32_t wl = static_cast<uint32_t>(wgt0) + sb * (kFB >> 4);
           if (kk == 0) {
             // first K-step of a tile: each accumulator as soon as it is drained
 #pragma unroll
             for (int h = 0; h < kFSlices; ++h) {
-              if (*abort_flag || !mbar_wait(&tempty[h], tph)) { ok = false; break; }
+              if (!wait(&tempty[h], tph)) { ok = false; break; }
               tc_fence_after();
               if (kLayer || h < nh) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mma(h, a0, b0, j, j > 0 ? 1u : 0u);
+                for (int j = 0; j < 4; ++j) mma(h, al + j * 2, wl + j * kWSlice, j > 0 ? 1u : 0u);
               }
             }
             if (!ok) break;
-          } else {
+          } else if (kLayer || nh == kFSlices) {
             // the two accumulators in turn: a product waits for the one before
             // it on the same accumulator (171 clocks from one to the next at N =
             // 256, 128 where two alternate)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-              for (int h = 0; h < kFSlices; ++h)
-                if (kLayer || h < nh) mma(h, a0, b0, j, 1u);
+              for (int h = 0; h < kFSlices; ++h) mma(h, al + j * 2, wl + j * kWSlice, 1u);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma(0, al + j * 2, wl + j * kWSlice, 1u);
           }
-          umma_commit_pair_mc(&empty_a[sa], 0x3);
-          umma_commit_pair_mc(&empty_b[sb], 0x3);
+          umma_commit_pair_mc_if(elected, smem_u32(&empty_a[sa]), 0x3);
+          umma_commit_pair_mc_if(elected, smem_u32(&empty_b[sb]), 0x3);
+          next_a();
+          if (++sb == kFBStages) { sb = 0; phb ^= 1; }
         }
         if (!ok) break;
         for (int l = 0; l < kLora; ++l) {   // LoRA steps
-          uint32_t s1, s2;
-          if (!wait_a(s1) || !wait_a(s2)) { ok = false; break; }
+          const uint32_t s1 = sa;
+          if (!wait(&full_a[s1], pha)) { ok = false; break; }
+          next_a();
+          const uint32_t s2 = sa;
+          if (!wait(&full_a[s2], pha)) { ok = false; break; }
+          next_a();
           tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + s1 * kFA), w0 = smem_u32(sA + s2 * kFA);
+          const uint32_t al = static_cast<uint32_t>(act0) + s1 * (kFA >> 4);
+          const uint32_t wl = static_cast<uint32_t>(lor0) + s2 * (kFA >> 4);
           for (int j = 0; j < args.rsteps; ++j)
 #pragma unroll
             for (int h = 0; h < kFSlices; ++h)
-              if (kLayer || h < nh) mma(h, a0, w0, j, 1u);
-          umma_commit_pair_mc(&empty_a[s1], 0x3);
-          umma_commit_pair_mc(&empty_a[s2], 0x3);
+              if (kLayer || h < nh) mma(h, al + j * 2, wl + j * kWSlice, 1u);
+          umma_commit_pair_mc_if(elected, smem_u32(&empty_a[s1]), 0x3);
+          umma_commit_pair_mc_if(elected, smem_u32(&empty_a[s2]), 0x3);
         }
         if (!ok) break;
-        umma_commit_pair_mc(tfull, 0x3);
+        umma_commit_pair_mc_if(elected, smem_u32(tfull), 0x3);
       }
       if (!ok) *abort_flag = 1;
-      umma_commit_pair_mc(drain, 0x1);
+      umma_commit_pair_mc_if(elected, smem_u32(drain), 0x1);
       (void)mbar_wait(drain, 0);
     }
   } else if (warp < 2 + kFDecAll) {
