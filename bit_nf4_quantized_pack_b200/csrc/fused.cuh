@@ -82,6 +82,9 @@ __constant__ float kNF4g[32] = {QNF4_TABLE_VALUES, QNF4_INT4_VALUES};
 // steps give each CTA the rows of its own B and zeros (a box past the
 // matrix's last row) in the other's step.  The gated backward runs through
 // the K-steps of dG·Ŵgᵀ and then of dU·Ŵuᵀ in the same accumulators.
+// Where dX has few tiles (few rows), a tile's K-steps are cut into `splits`
+// equal items; each leaves fp32 sums of its own, which split_join_kernel adds in
+// order.  The first item of a tile has its LoRA steps.
 // These modes and the loss's split activation rows as m0 + 256h + 128q and
 // leave out slice h = 1 where a tile has no more than 256 rows.
 // ===========================================================================
@@ -98,6 +101,8 @@ constexpr bool mode_transposed(int m) { return m == kModeBwd || m == kModeGatedB
 constexpr bool mode_gated(int m) { return m == kModeGatedFwd || m == kModeGatedBwd; }
 constexpr bool mode_loss(int m) { return m >= kModeLossStats; }
 constexpr int mode_lora_steps(int m) { return mode_loss(m) ? 0 : (mode_gated(m) ? 2 : 1); }
+// dX modes may split the contraction of a tile over several work items
+constexpr bool mode_splits(int m) { return m == kModeGatedBwd || m == kModeLossDX; }
 constexpr int mode_tile_cols(int m) { return m == kModeGatedFwd ? 128 : 256; }
 
 constexpr int kFAStages = 4;          // activation tiles (TMA)
@@ -134,10 +139,17 @@ struct FusedArgs {
   int32_t* d_status;
 };
 
+// Split contraction of the dX modes: K-steps per item (steps * splits >= nk),
+// and with splits > 1 the items' sums [splits][M][Nout].
+struct SplitArgs : FusedArgs {
+  int splits, steps;
+  float* part;
+};
+
 // What the gated modes need besides: the second weight (nk counts the K-steps
 // of both in the backward), and in the forward the activation and the buffers
 // that keep g and u for the backward (all null: nothing is kept).
-struct GatedArgs : FusedArgs {
+struct GatedArgs : SplitArgs {
   ScaleView sv2;
   const uint8_t* packed2;
   int act;
@@ -148,7 +160,7 @@ struct GatedArgs : FusedArgs {
 
 // What the loss modes need besides.  The weight's columns col0 .. col0 + Nout
 // are the piece; columns from `vocab` on do not exist for the softmax.
-struct LossArgs : FusedArgs {
+struct LossArgs : SplitArgs {
   int col0;
   int vocab;
   const int64_t* labels;
@@ -264,7 +276,13 @@ __device__ __forceinline__ RowFetch fetch_row(const typename ModeTypes<kMode>::A
   f.s2v = 1.0f;
   f.valid = false;
   f.second = false;
-  if (tile >= num_tiles || kk >= a.nk) return f;
+  if (tile >= num_tiles) return f;
+  if constexpr (mode_splits(kMode)) {
+    const int tiles = a.m_tiles * a.n_tiles, split = tile / tiles;
+    tile -= split * tiles;
+    kk += split * a.steps;
+  }
+  if (kk >= a.nk) return f;
   const int n0 = (tile / a.m_tiles) * mode_tile_cols(kMode);
   const int64_t rowbytes = a.Nw / 2;
   const int64_t bpr = a.Nw / 64;
@@ -508,22 +526,67 @@ __device__ __forceinline__ void epilogue_loss_grad(const LossArgs& a, uint32_t t
 }
 
 // dX of one output column (this lane) over 32 rows, added to the pieces
-// before this one in fp32; the last piece rounds to bf16.
+// before this one in fp32 (without a result, so that no load waits between
+// stores); the last piece adds the sums and rounds to bf16.
 __device__ __forceinline__ void epilogue_loss_dx(const LossArgs& a, const uint32_t (&v)[32], int col, int row0) {
   if (col >= a.Nout || row0 >= a.M) return;
   const int64_t ld = a.Nout;
   const int64_t at = row0 * ld + col;
   const int nrows = a.M - row0;
+  if (!a.last) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    if (i < nrows) {
-      float x = __uint_as_float(v[i]);
-      if (!a.first) x += a.acc[at + i * ld];
-      if (a.last)
-        a.out[at + i * ld] = static_cast<uint16_t>(pack_bf16x2(x, 0.0f));
-      else
-        a.acc[at + i * ld] = x;
+    for (int i = 0; i < 32; ++i)
+      if (i < nrows) {
+        if (a.first)
+          a.acc[at + i * ld] = __uint_as_float(v[i]);
+        else
+          atomicAdd(a.acc + at + i * ld, __uint_as_float(v[i]));   // one thread per element: no order
+      }
+    return;
+  }
+  float old[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) old[i] = !a.first && i < nrows ? a.acc[at + i * ld] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i < nrows)
+      a.out[at + i * ld] = static_cast<uint16_t>(pack_bf16x2(__uint_as_float(v[i]) + old[i], 0.0f));
+}
+
+// A split item's fp32 sums of one output column over 32 rows; false where the
+// tile is not split.
+__device__ __forceinline__ bool split_sums(const SplitArgs& a, const uint32_t (&v)[32], int split, int col,
+                                           int row0) {
+  if (a.splits <= 1) return false;
+  if (col < a.Nout && row0 < a.M) {
+    const int64_t ld = a.Nout;
+    float* dst = a.part + (static_cast<int64_t>(split) * a.M + row0) * ld + col;
+    const int nrows = a.M - row0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < nrows) dst[i * ld] = __uint_as_float(v[i]);
+  }
+  return true;
+}
+__device__ __forceinline__ bool split_sums(const FusedArgs&, const uint32_t (&)[32], int, int, int) { return false; }
+
+// The split items' sums, in order, rounded to bf16 (four elements a thread).
+__global__ void __launch_bounds__(256)
+    split_join_kernel(const float4* __restrict__ part, int splits, int64_t quads, uint2* __restrict__ out) {
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < quads;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    float4 s = part[i];
+#pragma unroll 4
+    for (int k = 1; k < splits; ++k) {
+      const float4 v = part[k * quads + i];
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
     }
+    out[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   }
 }
 
@@ -588,7 +651,21 @@ __global__ void __launch_bounds__(kFThreads, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int num_tiles = args.m_tiles * args.n_tiles;
+  // work items: the tiles, or `splits` of each (item i: tile i % tiles)
+  const int tiles = args.m_tiles * args.n_tiles;
+  int num_tiles = tiles, nsteps = args.nk;
+  if constexpr (mode_splits(kMode)) {
+    num_tiles *= args.splits;
+    nsteps = args.steps;
+  }
+  auto split_of = [&](int& item) -> int {
+    if constexpr (mode_splits(kMode)) {
+      const int s = item / tiles;
+      item -= s * tiles;
+      return s;
+    }
+    return 0;
+  };
   pdl_launch_dependents();   // after this CTA holds its TMEM
   // the loss modes have no rank-r product before them: every input may come
   // from the kernel that precedes
@@ -633,12 +710,17 @@ __global__ void __launch_bounds__(kFThreads, 1)
         return kMode == kModeFwd ? m0 + 256 * rank + 128 * h : m0 + 256 * h + 128 * rank;
       };
       bool lora_ready = false;
-      for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+      for (int item = pair; item < num_tiles && ok; item += npairs) {
+        int tile = item;
+        const int split = split_of(tile);
         const int m0 = (tile % args.m_tiles) * kFPairRows;
         const int n0 = (tile / args.m_tiles) * kTileCols;
         const int nh = tile_slices<kMode>(args.M, m0);
         const uint32_t act_bytes = kLayer ? kFA : static_cast<uint32_t>(nh) * 16384u;
-        for (int kk = 0; kk < args.nk && ok; ++kk) {
+        // (steps past the contraction's end multiply zeros by zeros: boxes past
+        // the end arrive as zero fill, and so do the decoders' rows)
+        const int kk0 = split * nsteps;
+        for (int kk = kk0; kk < kk0 + nsteps && ok; ++kk) {
           uint32_t s;
           if (!take(s, act_bytes)) { ok = false; break; }
           uint8_t* a = sA + s * kFA;
@@ -656,6 +738,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         }
         if (!ok) break;
         // LoRA steps: Zc / dZ into one stage, B / A into the next
+        if (split > 0) continue;
         if (kLora > 0 && !lora_ready) {
           pdl_wait();   // Zc (dZ) is the preceding kernel's output
           lora_ready = true;
@@ -731,10 +814,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
         else
           umma_bf16_pair_lo(elected, tmem + h * kFAccCols, al + h * 1024, acthi, wl, wgthi, idesc, accum);
       };
-      for (int tile = pair; tile < num_tiles && ok; tile += npairs, ++tc) {
+      for (int item = pair; item < num_tiles && ok; item += npairs, ++tc) {
+        int tile = item;
+        const int split = split_of(tile);
         const uint32_t tph = (tc & 1) ^ 1;       // parity of the previous tile's release
         const int nh = tile_slices<kMode>(args.M, (tile % args.m_tiles) * kFPairRows);
-        for (int kk = 0; kk < args.nk; ++kk) {
+        for (int kk = 0; kk < nsteps; ++kk) {
           if (!wait(&full_a[sa], pha) || !wait(&full_b[sb], phb)) { ok = false; break; }
           tc_fence_after();
           const uint32_t al = static_cast<uint32_t>(act0) + sa * (kFA >> 4);
@@ -769,7 +854,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
           if (++sb == kFBStages) { sb = 0; phb ^= 1; }
         }
         if (!ok) break;
-        for (int l = 0; l < kLora; ++l) {   // LoRA steps
+        for (int l = 0; l < kLora && split == 0; ++l) {   // LoRA steps
           const uint32_t s1 = sa;
           if (!wait(&full_a[s1], pha)) { ok = false; break; }
           next_a();
@@ -807,7 +892,6 @@ __global__ void __launch_bounds__(kFThreads, 1)
     if constexpr (kMode == kModeGatedBwd) {
       if (args.sv2.code8 != nullptr) off2 = __ldg(args.sv2.offset);
     }
-    const int nsteps = args.nk;                // decoded steps per tile
     bool ok = true;
     int tile = pair, kk = 0;                   // the step being decoded
     advance(tile, kk, grp, nsteps, npairs);
@@ -876,7 +960,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
     uint32_t tc = 0;
     bool ok = true;
     const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);   // CTA 0's release barriers
-    for (int tile = pair; tile < num_tiles && ok; tile += npairs, ++tc) {
+    for (int item = pair; item < num_tiles && ok; item += npairs, ++tc) {
+      int tile = item;
+      const int split = split_of(tile);
       const int m0 = (tile % args.m_tiles) * kFPairRows;
       const int n0 = (tile / args.m_tiles) * kTileCols;
       const int nh = tile_slices<kMode>(args.M, m0);
@@ -901,7 +987,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
           uint32_t v[32];
           tmem_ld_32x32b_x32(tbase + c * 32, v);
           tmem_ld_wait();
-          if constexpr (kMode == kModeLossDX) {
+          if (mode_splits(kMode) && split_sums(args, v, split, n0 + 128 * rank + q * 32 + lane,
+                                               m0 + h * kFAccCols + c * 32)) {
+          } else if constexpr (kMode == kModeLossDX) {
             epilogue_loss_dx(args, v, n0 + 128 * rank + q * 32 + lane, m0 + h * kFAccCols + c * 32);
           } else if (!kBwd) {
             // lane = output row, 32 consecutive output columns
@@ -951,6 +1039,52 @@ __global__ void __launch_bounds__(kFThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
+}
+
+// Items a dX tile is cut into: as many as keep every pair of the sizing SM
+// count busy, of at least kSplitSteps K-steps each (an item's start and its
+// sums cost about as much as four steps).
+constexpr int kSplitSteps = 8;
+constexpr int kSizingPairs = 74;
+inline int dx_most_splits(int tiles, int nk) {
+  const int s = kSizingPairs / tiles, m = nk / kSplitSteps;
+  const int most = s < m ? s : m;
+  return most < 2 ? 1 : most;
+}
+inline int dx_splits(int tiles, int nk) {
+  const int s = dx_most_splits(tiles, nk);   // equal items may need fewer
+  const int steps = (nk + s - 1) / s;
+  return (nk + steps - 1) / steps;
+}
+
+// Workspace of a split dX (M x cols), 0 when it is not split.  Grows with nk, so
+// that a size asked for with more K-steps serves fewer.
+inline size_t split_bytes(int64_t M, int64_t cols, int64_t nk) {
+  const int64_t tiles = ((M + kFPairRows - 1) / kFPairRows) * ((cols + kFPairCols - 1) / kFPairCols);
+  if (tiles > kSizingPairs) return 0;
+  const int s = dx_most_splits(static_cast<int>(tiles), static_cast<int>(nk));
+  return s > 1 ? (static_cast<size_t>(s) * M * cols * 4 + 255) / 256 * 256 : 0;
+}
+
+// Fills the split of a dX launch; `part` from split_bytes (null: not split).
+inline void set_split(SplitArgs& a, float* part) {
+  const int tiles = a.m_tiles * a.n_tiles;
+  a.splits = part != nullptr ? dx_splits(tiles, a.nk) : 1;
+  a.steps = (a.nk + a.splits - 1) / a.splits;
+  a.part = part;
+}
+
+inline cudaError_t launch_split_join(const SplitArgs& a, int prof_kind, cudaStream_t st) {
+  const int64_t quads = static_cast<int64_t>(a.M) * a.Nout / 4;
+  const int64_t want = (quads + 255) / 256;
+  cudaError_t e;
+  {
+    ProfScope prof(prof_kind, st);
+    e = launch_pdl(split_join_kernel, dim3(static_cast<unsigned>(want < 1184 ? want : 1184)), dim3(256), 0, st, 1,
+                   reinterpret_cast<const float4*>(a.part), a.splits, quads, reinterpret_cast<uint2*>(a.out));
+  }
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
 }
 
 template <int kMode>

@@ -108,8 +108,9 @@ size_t gated_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r) {
 
 size_t gated_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r) {
   const int rp = padded_rank(r);
-  // dG, dU; dZg, dZu; when r is not a multiple of 8 padded copies of Zg, Zu, Ag, Au
-  return 2 * align256(static_cast<size_t>(M) * N * 2) + 2 * align256(static_cast<size_t>(M) * rp * 2) +
+  // dG, dU; dZg, dZu; a split dX's sums; when r is not a multiple of 8 padded
+  // copies of Zg, Zu, Ag, Au
+  return split_bytes(M, K, 2 * (N / 64)) + 2 * align256(static_cast<size_t>(M) * N * 2) + 2 * align256(static_cast<size_t>(M) * rp * 2) +
          (rp != r ? 2 * align256(static_cast<size_t>(M) * rp * 2) + 2 * align256(static_cast<size_t>(K) * rp * 2)
                   : 0);
 }
@@ -212,6 +213,8 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
     Apg = bf16_rows(K, rp);
     Apu = bf16_rows(K, rp);
   }
+  const size_t split = split_bytes(M, K, 2 * (N / 64));
+  float* part = split > 0 ? static_cast<float*>(cur.take(split)) : nullptr;
   if (!cur.ok) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   const uint16_t *Ag = w.Ag, *Au = w.Au, *Zg = kept.Zg, *Zu = kept.Zu;
@@ -271,10 +274,11 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   ga.packed2 = w.packed_u;
   ga.out = dX;
   ga.d_status = d_status;
+  set_split(ga, part);
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int grid = fused_pairs(ga.m_tiles * ga.n_tiles, sms);
+  const int grid = fused_pairs(ga.m_tiles * ga.n_tiles * ga.splits, sms);
   // operands of dA and dB, read transposed
   CUtensorMap tXmn, tdZg, tdZu, tGmn, tUmn, tZg, tZu;
   if (X8 == nullptr && !make_tmap_2d(&tXmn, X, kBF16, 2, M, K, K, 64, 64, kSW128)) return cudaErrorInvalidValue;
@@ -298,6 +302,7 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
                         maps, ga);
   }
   if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess && ga.splits > 1) e = launch_split_join(ga, kProfGated, st);
   if (s2 != st) {
     const cudaError_t ew = cudaStreamWaitEvent(s2, ss->fork, 0);
     if (ew != cudaSuccess) {

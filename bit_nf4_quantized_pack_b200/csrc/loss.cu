@@ -98,16 +98,18 @@ cudaError_t run_loss(const CUtensorMap& act, LossArgs a, int nk, int64_t cols, c
   a.nk = nk;
   a.Nout = static_cast<int>(cols);
   a.n_tiles = static_cast<int>((cols + kFPairCols - 1) / kFPairCols);
+  set_split(a, a.part);
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   {
     ProfScope prof(kProfLoss, st);
-    e = launch_pdl_pair(fused_nf4_gemm_kernel<kMode>, dim3(2 * fused_pairs(a.m_tiles * a.n_tiles, sms)),
+    e = launch_pdl_pair(fused_nf4_gemm_kernel<kMode>, dim3(2 * fused_pairs(a.m_tiles * a.n_tiles * a.splits, sms)),
                         dim3(kFThreads), kFSmem, st, typename ModeTypes<kMode>::Maps{act}, a);
   }
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess && a.splits > 1) e = launch_split_join(a, kProfLoss, st);
+  return e;
 }
 
 }  // namespace
@@ -119,8 +121,9 @@ size_t loss_fwd_workspace_bytes(int64_t M, int64_t N) {
 
 size_t loss_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   const int64_t per = piece_cols(M, N);
+  // P; the pieces' sums, or with one piece a split dX's
   return align256(static_cast<size_t>(M) * per * 2) +
-         (per < N ? align256(static_cast<size_t>(M) * K * 4) : 0);
+         (per < N ? align256(static_cast<size_t>(M) * K * 4) : split_bytes(M, K, N / 64));
 }
 
 cudaError_t launch_loss_fwd(int64_t M, int64_t K, int64_t N, int64_t vocab, const uint16_t* X,
@@ -162,6 +165,9 @@ cudaError_t launch_loss_bwd(int64_t M, int64_t K, int64_t N, int64_t vocab, cons
   const int64_t per = piece_cols(M, N);
   uint16_t* P = static_cast<uint16_t*>(cur.take(static_cast<size_t>(M) * per * 2));
   float* acc = per < N ? static_cast<float*>(cur.take(static_cast<size_t>(M) * K * 4)) : nullptr;
+  // (split by the vocabulary's steps, which are no more than the head's)
+  const size_t split = per < N ? 0 : split_bytes(M, K, (vocab + 63) / 64);
+  float* part = split > 0 ? static_cast<float*>(cur.take(split)) : nullptr;
   if (!cur.ok) return cudaErrorInvalidValue;
   CUtensorMap tX;
   if (!make_tmap_2d(&tX, X, kBF16, 2, M, K, K, 64, 128, kSW128)) return cudaErrorInvalidValue;
@@ -179,6 +185,7 @@ cudaError_t launch_loss_bwd(int64_t M, int64_t K, int64_t N, int64_t vocab, cons
     CUtensorMap tP;
     if (!make_tmap_2d(&tP, P, kBF16, 2, M, cols, cols, 64, 128, kSW128)) return cudaErrorInvalidValue;
     a.out = dX;
+    a.part = part;
     a.acc = acc;
     a.first = c0 == 0 ? 1 : 0;
     a.last = c0 + cols >= end ? 1 : 0;
