@@ -27,7 +27,7 @@ import torch
 
 from . import _args, _lib
 from ._lib import NF4StateC, QLoRAError, check, lib
-from .act8 import Act8, act8_dequantize, act8_quantize, check_act8
+from .act8 import Act8, act8_dequantize, act8_quantize, act8_struct
 from .gated import GatedSaved, gated_backward, gated_forward
 from .loss import head_loss_backward, head_loss_forward
 
@@ -366,39 +366,30 @@ def linear_backward(dY, X, Zc, w: NF4Weight, A, B, c: float, *, dX=None, dA=None
 def _linear_backward_act8(dY, X, Zc, w, A, B, c, dX, dA, dB, status, workspace, grad_dtype):
     """linear_backward through qlora_linear_bwd_act8."""
     M, N, dev = _args.cuda_2d(dY, "dY")
+    gcode = _args.grad_code(grad_dtype)
     is8 = isinstance(X, Act8)
     K = X.shape[1] if (is8 or isinstance(X, torch.Tensor)) and len(X.shape) == 2 else -1
-    if is8:
-        check_act8(X, "X", (M, K), dev)
-        if Zc is None:
-            raise ValueError("the backward from an 8-bit input needs the forward's Zc")
-    else:
-        _args.tensor(X, "X", (M, K), dev)
-    gcode = _args.grad_code(grad_dtype)
-    _args.weight(w, "w", (K, N), dev)
+    x8 = act8_struct(X, "X", M, K, dev) if is8 else None
+    x16 = None if is8 else _args.tensor(X, "X", (M, K), dev)
+    if is8 and Zc is None:
+        raise ValueError("the backward from an 8-bit input needs the forward's Zc")
+    st = _args.weight(w, "w", K, N, dev)
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
         raise TypeError("A must be a matrix")
     r = A.shape[1]
-    _args.tensor(A, "A", (K, r), dev)
-    _args.tensor(B, "B", (r, N), dev)
-    if Zc is not None:
-        _args.tensor(Zc, "Zc", (M, r), dev)
+    pa, pb = _args.tensor(A, "A", (K, r), dev), _args.tensor(B, "B", (r, N), dev)
+    zc = None if Zc is None else _args.tensor(Zc, "Zc", (M, r), dev)
     with _args.on(dev):
-        out = []
-        for t, name, shape, dt in ((dX, "dX", (M, K), torch.bfloat16), (dA, "dA", (K, r), grad_dtype),
-                                   (dB, "dB", (r, N), grad_dtype)):
-            if t is None:
-                t = torch.empty(shape, dtype=dt, device=dev)
-            else:
-                _args.tensor(t, name, shape, dev, dt)
-            out.append(t)
-        ws = _args.workspace(workspace, lib.qlora_linear_bwd_workspace_size(M, K, N, r), dev)
+        dX = _args.output(dX, dY, "dX", (M, K))
+        dA = _args.output(dA, dY, "dA", (K, r), grad_dtype)
+        dB = _args.output(dB, dY, "dB", (r, N), grad_dtype)
+        ws = _args.workspace(workspace, lib.qlora_linear_bwd_workspace_size(M, K, N, r), dY)
         own = status is None
         status = new_status(dev) if own else status
-        check(lib.qlora_linear_bwd_act8(M, K, N, r, dY.data_ptr(), None if is8 else X.data_ptr(),
-                                        C.byref(X.cstruct()) if is8 else None, _args.ptr(Zc),
-                                        C.byref(w.cstruct()), A.data_ptr(), B.data_ptr(), float(c),
-                                        *(t.data_ptr() for t in out), gcode, ws.data_ptr(), ws.numel(),
-                                        status.data_ptr(), _args.stream(dev)), "qlora_linear_bwd_act8")
-        _finish(status, own, "qlora_linear_bwd_act8")
-    return tuple(out)
+        check(lib.qlora_linear_bwd_act8(M, K, N, r, dY.data_ptr(), x16, C.byref(x8) if is8 else None, zc,
+                                        C.byref(st), pa, pb, c, dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), gcode,
+                                        ws.data_ptr(), ws.numel(), status.data_ptr(), _args.stream(dev)),
+              "qlora_linear_bwd_act8")
+        if own:
+            _finish(status, own, "qlora_linear_bwd_act8")
+    return dX, dA, dB

@@ -12,7 +12,7 @@ import contextlib
 
 import torch
 
-from ._lib import QLORA_DTYPE_BF16, QLORA_DTYPE_F32
+from ._lib import QLORA_DTYPE_BF16, QLORA_DTYPE_F32, NF4StateC
 
 GRAD_DTYPES = {torch.float32: QLORA_DTYPE_F32, torch.bfloat16: QLORA_DTYPE_BF16}
 
@@ -38,41 +38,52 @@ def stream(dev):
 
 def cuda_2d(t, name):
     """A contiguous 2-D CUDA bf16 tensor; returns its shape and device."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous CUDA bfloat16 tensor")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must have two dimensions")
-    return t.shape[0], t.shape[1], t.device
+    return shape[0], shape[1], t.device
 
 
 def tensor(t, name, shape, dev, dtype=torch.bfloat16):
-    """A contiguous tensor of `shape` and `dtype` on `dev`."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+    """The address of a contiguous tensor of `shape` and `dtype` on `dev`."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} tensor on {dev}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def weight(w, name, shape, dev):
-    """An NF4Weight of `shape` whose buffers hold what its struct promises."""
-    if tuple(w.shape) != shape:
-        raise ValueError(f"{name} must be {shape[0]} x {shape[1]}, not {tuple(w.shape)}")
-    numel = shape[0] * shape[1]
+def weight(w, name, K, N, dev):
+    """The C struct of an NF4Weight of K x N whose buffers hold what it promises."""
+    shape = w.shape
+    if len(shape) != 2 or shape[0] != K or shape[1] != N:
+        raise ValueError(f"{name} must be {K} x {N}, not {tuple(shape)}")
+    numel = K * N
     n1 = (numel + 63) // 64
-    _buffer(w.packed, torch.uint8, (numel + 1) // 2, name, dev)
+    packed = _buffer(w.packed, torch.uint8, (numel + 1) // 2, name, dev)
     if w.double_quant:
-        _buffer(w.code8, torch.uint8, n1, name, dev)
-        _buffer(w.s2, torch.float32, (n1 + 255) // 256, name, dev)
-        _buffer(w.offset, torch.float32, 1, name, dev)
-    else:
-        _buffer(w.absmax, torch.float32, n1, name, dev)
+        return NF4StateC(numel, 64, 1, 256, w.codebook, packed, None, _buffer(w.code8, torch.uint8, n1, name, dev),
+                         _buffer(w.s2, torch.float32, (n1 + 255) // 256, name, dev),
+                         _buffer(w.offset, torch.float32, 1, name, dev))
+    return NF4StateC(numel, 64, 0, 256, w.codebook, packed, _buffer(w.absmax, torch.float32, n1, name, dev))
 
 
 def _buffer(t, dtype, n, name, dev):
-    if t is None or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
         raise TypeError(f"{name}: a buffer is missing, or not a contiguous {dtype} tensor on {dev}")
     if t.numel() != n:
         raise ValueError(f"{name}: a buffer has {t.numel()} elements, not {n}")
+    return t.data_ptr()
+
+
+def output(t, like, name, shape, dtype=torch.bfloat16):
+    """`t` checked, or a new tensor of `shape` and `dtype` beside `like`."""
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    tensor(t, name, shape, like.device, dtype)
+    return t
 
 
 def grad_code(dtype):
@@ -81,16 +92,13 @@ def grad_code(dtype):
     return GRAD_DTYPES[dtype]
 
 
-def ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def workspace(given, nbytes, dev):
+def workspace(given, nbytes, like):
     """The caller's workspace, or a new one from the caching allocator: it is
     ordered on the current stream, and under graph capture it belongs to that
     graph's own pool, so no two captured graphs or streams ever share one."""
     if given is None:
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        return like.new_empty((max(nbytes, 256),), dtype=torch.uint8)
+    dev = like.device
     if (not isinstance(given, torch.Tensor) or given.dtype != torch.uint8 or given.device != dev
             or not given.is_contiguous()):
         raise TypeError(f"workspace must be a contiguous uint8 tensor on {dev}")

@@ -43,12 +43,17 @@ class Act8:
         return Act8C(self.codes.shape[0], self.codes.shape[1], self.codes.data_ptr(), self.scales.data_ptr())
 
 
-def check_act8(a, name, shape, dev):
-    """`a` is an Act8 of `shape` on `dev`, with buffers of the right extents."""
+def act8_struct(a, name, M, K, dev):
+    """The C struct of an Act8 of M x K on `dev` with buffers of the right extents."""
     if not isinstance(a, Act8):
         raise TypeError(f"{name} must be an Act8")
-    _args.tensor(a.codes, f"{name}.codes", shape, dev, torch.int8)
-    _args.tensor(a.scales, f"{name}.scales", (shape[0], shape[1] // 64), dev, torch.float32)
+    return Act8C(M, K, _args.tensor(a.codes, f"{name}.codes", (M, K), dev, torch.int8),
+                 _args.tensor(a.scales, f"{name}.scales", (M, K // 64), dev, torch.float32))
+
+
+def new_act8(M, K, like):
+    """Buffers for an Act8 of M x K beside `like`."""
+    return Act8(like.new_empty((M, K), dtype=torch.int8), like.new_empty((M, K // 64), dtype=torch.float32))
 
 
 def act8_quantize(X: torch.Tensor, *, out: Act8 | None = None, status: torch.Tensor | None = None) -> Act8:
@@ -58,15 +63,14 @@ def act8_quantize(X: torch.Tensor, *, out: Act8 | None = None, status: torch.Ten
     M, K, dev = _args.cuda_2d(X, "X")
     with _args.on(dev):
         if out is None:
-            out = Act8.empty(M, K, dev)
-        else:
-            check_act8(out, "out", (M, K), dev)
+            out = new_act8(M, K, X)
+        st = act8_struct(out, "out", M, K, dev)
         own = status is None
         status = new_status(dev) if own else status
-        st = out.cstruct()
         check(lib.qlora_act8_quantize(X.data_ptr(), C.byref(st), status.data_ptr(), _args.stream(dev)),
               "qlora_act8_quantize")
-        _finish(status, own, "qlora_act8_quantize")
+        if own:
+            _finish(status, own, "qlora_act8_quantize")
     return out
 
 
@@ -74,13 +78,10 @@ def act8_dequantize(a: Act8, *, out: torch.Tensor | None = None) -> torch.Tensor
     """The bf16 matrix that the checkpoint stands for."""
     if not isinstance(a, Act8) or not a.codes.is_cuda or a.codes.dim() != 2:
         raise TypeError("a must be an Act8 on a CUDA device")
+    M, K = a.codes.shape
     dev = a.device
-    check_act8(a, "a", tuple(a.codes.shape), dev)
+    st = act8_struct(a, "a", M, K, dev)
     with _args.on(dev):
-        if out is None:
-            out = torch.empty(a.codes.shape, dtype=torch.bfloat16, device=dev)
-        else:
-            _args.tensor(out, "out", a.codes.shape, dev)
-        st = a.cstruct()
+        out = _args.output(out, a.codes, "out", (M, K))
         check(lib.qlora_act8_dequantize(C.byref(st), out.data_ptr(), _args.stream(dev)), "qlora_act8_dequantize")
     return out

@@ -57,19 +57,48 @@ __device__ __forceinline__ float act_value_grad(int act, float g, float& d) {
 // all-zero block among them); code q = rint(fl32(x / s)), ties to even;
 // value = bf16(fl32(q * s)).
 // ---------------------------------------------------------------------------
+// fl32(amax / 127) for a bf16 amax: the product with the rounded reciprocal and
+// one exact remainder (equal to the division for every finite bf16 magnitude
+// whose quotient is normal, by enumeration; smaller ones give 1 either way).
 __device__ __forceinline__ float act8_scale(float amax) {
-  const float s = __fdiv_rn(amax, 127.0f);
+  constexpr float r = 1.0f / 127.0f;
+  const float q = __fmul_rn(amax, r);
+  const float s = __fmaf_rn(__fmaf_rn(-127.0f, q, amax), r, q);
   return s >= FLT_MIN ? s : 1.0f;
 }
+// a factor for act8_round: 1 / s within 2^-23
+__device__ __forceinline__ float act8_inverse(float s) { return __fdividef(1.0f, s); }
 
-// rint(fl32(x / s)).  x * inv is within 127 * 2^-22 of x / s (two roundings of
-// a magnitude of at most 127), so the two round alike unless the product is
-// within 2^-14 of a tie; only then is the division carried out.
-__device__ __forceinline__ int act8_code(float x, float s, float inv) {
+// rint(fl32(x / s)), in two steps.  x * inv is within 127 * 2^-22 of x / s (the
+// inverse's error and one rounding, of a magnitude of at most 127), so both round alike unless the
+// product is within 2^-14 of a tie: act8_round rounds it (by the addition of 1.5
+// * 2^23, whose low byte then holds the code) and notes a near tie, and only for
+// a block of values with one does act8_exact carry the divisions out.
+constexpr float kAct8Magic = 12582912.0f;
+__device__ __forceinline__ uint32_t act8_round(float x, float inv, bool& near) {
   const float t = x * inv;
-  float q = rintf(t);
-  if (fabsf(fabsf(t - q) - 0.5f) < 6.103515625e-05f) q = rintf(__fdiv_rn(x, s));
-  return static_cast<int>(q);
+  const float r = __fadd_rn(t, kAct8Magic);
+  near |= fabsf(__fadd_rn(t, -__fadd_rn(r, -kAct8Magic))) > 0.5f - 6.103515625e-05f;
+  return __float_as_uint(r);
+}
+__device__ __forceinline__ uint32_t act8_exact(float x, float s) {
+  return __float_as_uint(__fadd_rn(rintf(__fdiv_rn(x, s)), kAct8Magic));
+}
+// four results of these as four code bytes
+__device__ __forceinline__ uint32_t act8_pack(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+// the codes of four values
+__device__ __forceinline__ uint32_t act8_codes4(const float (&x)[4], float s, float inv) {
+  bool near = false;
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = act8_round(x[i], inv, near);
+  if (near) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = act8_exact(x[i], s);
+  }
+  return act8_pack(r[0], r[1], r[2], r[3]);
 }
 
 // The code's value before its rounding to bf16.

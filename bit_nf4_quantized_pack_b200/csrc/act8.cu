@@ -1,12 +1,11 @@
 // 8-bit activation checkpoints: the codec (see act.cuh for its arithmetic).
 //
 // Both directions stream: 2 B + 1 B and a 64th of 4 B per element, so HBM
-// bounds them.  Eight lanes share a block of 64: each loads 16 bytes (eight
-// bf16), the block's largest magnitude crosses the eight lanes in three
-// shuffles of packed 16-bit maxima (bf16 magnitudes order as integers, NaN
-// and infinity above all finite values), and each lane stores its eight codes
-// as 8 bytes.  A thread takes kUnroll such pieces at once so that as many
-// loads are in flight.
+// bounds them.  Quantize: four lanes share a block of 64, each with sixteen
+// elements (two 16-byte loads, one 16-byte store), so that a block's scale is
+// formed four times and its largest magnitude crosses lanes in two shuffles of
+// packed 16-bit maxima (bf16 magnitudes order as integers, NaN and infinity
+// above all finite values).
 #include "act.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
@@ -17,50 +16,51 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
+constexpr int kQUnroll = 2;
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-
+// `pieces` of sixteen elements, a multiple of 4
 __global__ void __launch_bounds__(kThreads)
-    act8_quantize_kernel(const uint4* __restrict__ X, int64_t pieces, uint2* __restrict__ codes,
+    act8_quantize_kernel(const uint4* __restrict__ X, int64_t pieces, uint4* __restrict__ codes,
                          float* __restrict__ scales, int32_t* d_status) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
   bool bad = false;
-  // `pieces` is a multiple of 8, so a block's eight lanes enter together; the
-  // warp leaves the loop together once its first lane is past the end
+  // a block's four lanes enter together; the warp leaves the loop together once
+  // its first lane is past the end
   for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i0 - lane < pieces;
-       i0 += stride * kUnroll) {
-    uint4 x[kUnroll];
+       i0 += stride * kQUnroll) {
+    uint4 x[kQUnroll][2];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kQUnroll; ++u) {
       const int64_t i = i0 + u * stride;
-      x[u] = i < pieces ? __ldcs(X + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) x[u][h] = i < pieces ? __ldcs(X + 2 * i + h) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kQUnroll; ++u) {
       const int64_t i = i0 + u * stride;
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      const uint32_t w[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
       uint32_t m = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) m = max_u16x2(m, w[k] & 0x7FFF7FFFu);
-#pragma unroll
-      for (int d = 1; d < 8; d <<= 1) m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+      for (int k = 0; k < 8; ++k) m = __vmaxu2(m, w[k] & 0x7FFF7FFFu);
+      m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
       const uint32_t top = max(m & 0xFFFFu, m >> 16);
       bad |= top >= 0x7F80u;
       const float s = act8_scale(__uint_as_float(top << 16));
-      const float inv = __frcp_rn(s);
-      uint32_t o[2] = {0, 0};
+      const float inv = act8_inverse(s);
+      uint32_t o[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = static_cast<uint32_t>(act8_code(__uint_as_float(w[k] << 16), s, inv)) & 0xFFu;
-        const uint32_t hi = static_cast<uint32_t>(act8_code(__uint_as_float(w[k] & 0xFFFF0000u), s, inv)) & 0xFFu;
-        o[k >> 1] |= (lo | (hi << 8)) << (16 * (k & 1));
+        const float v[4] = {__uint_as_float(w[2 * k] << 16), __uint_as_float(w[2 * k] & 0xFFFF0000u),
+                            __uint_as_float(w[2 * k + 1] << 16), __uint_as_float(w[2 * k + 1] & 0xFFFF0000u)};
+        o[k] = act8_codes4(v, s, inv);
       }
       if (i < pieces) {
-        codes[i] = make_uint2(o[0], o[1]);
-        if ((lane & 7) == 0) scales[i >> 3] = s;
+        codes[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        if ((lane & 3) == 0) scales[i >> 2] = s;
       }
     }
   }
@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-unsigned grid_for(int64_t pieces, int num_sms) {
-  const int64_t want = (pieces + kThreads * kUnroll - 1) / (kThreads * kUnroll);
+unsigned grid_for(int64_t pieces, int unroll, int num_sms) {
+  const int64_t want = (pieces + kThreads * unroll - 1) / (kThreads * unroll);
   const int64_t most = static_cast<int64_t>(num_sms) * 8;
   return static_cast<unsigned>(want < most ? want : most);
 }
@@ -108,12 +108,12 @@ unsigned grid_for(int64_t pieces, int num_sms) {
 
 cudaError_t launch_act8_quantize(const uint16_t* X, int64_t numel, int8_t* codes, float* scales,
                                  int32_t* d_status, cudaStream_t st, int num_sms) {
-  const int64_t pieces = numel / 8;
+  const int64_t pieces = numel / 16;
   cudaError_t e;
   {
     ProfScope prof(kProfAct8, st);
-    e = launch_pdl(act8_quantize_kernel, dim3(grid_for(pieces, num_sms)), dim3(kThreads), 0, st, 1,
-                   reinterpret_cast<const uint4*>(X), pieces, reinterpret_cast<uint2*>(codes), scales,
+    e = launch_pdl(act8_quantize_kernel, dim3(grid_for(pieces, kQUnroll, num_sms)), dim3(kThreads), 0, st, 1,
+                   reinterpret_cast<const uint4*>(X), pieces, reinterpret_cast<uint4*>(codes), scales,
                    d_status);
   }
   if (e != cudaSuccess) return e;
@@ -126,7 +126,7 @@ cudaError_t launch_act8_dequantize(const int8_t* codes, const float* scales, int
   cudaError_t e;
   {
     ProfScope prof(kProfAct8, st);
-    e = launch_pdl(act8_dequantize_kernel, dim3(grid_for(pieces, num_sms)), dim3(kThreads), 0, st, 1,
+    e = launch_pdl(act8_dequantize_kernel, dim3(grid_for(pieces, kUnroll, num_sms)), dim3(kThreads), 0, st, 1,
                    reinterpret_cast<const uint2*>(codes), scales, pieces, reinterpret_cast<uint4*>(X));
   }
   if (e != cudaSuccess) return e;

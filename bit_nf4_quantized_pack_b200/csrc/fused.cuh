@@ -385,7 +385,7 @@ __device__ __forceinline__ void store_act8_block(uint32_t taddr, bool in, int8_t
     for (int i = 0; i < 32; ++i) amax = fmax_nan(amax, fabsf(round_bf16(__uint_as_float(v[i]))));
   }
   const float s = act8_scale(amax);
-  const float inv = __frcp_rn(s);
+  const float inv = act8_inverse(s);
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
     uint32_t v[32];
@@ -396,11 +396,9 @@ __device__ __forceinline__ void store_act8_block(uint32_t taddr, bool in, int8_t
       uint32_t w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        w[i] = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[i] |= (static_cast<uint32_t>(act8_code(round_bf16(__uint_as_float(v[4 * i + j])), s, inv)) & 0xFFu)
-                  << (8 * j);
+        const float x[4] = {round_bf16(__uint_as_float(v[4 * i])), round_bf16(__uint_as_float(v[4 * i + 1])),
+                            round_bf16(__uint_as_float(v[4 * i + 2])), round_bf16(__uint_as_float(v[4 * i + 3]))};
+        w[i] = act8_codes4(x, s, inv);
       }
       uint4* d = reinterpret_cast<uint4*>(codes + c * 32);
       d[0] = make_uint4(w[0], w[1], w[2], w[3]);

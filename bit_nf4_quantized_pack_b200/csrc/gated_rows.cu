@@ -582,10 +582,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       float amax = fmax_nan(fabsf(x0), fabsf(x1));
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) amax = fmax_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-      const float s = act8_scale(amax), inv = __frcp_rn(s);
-      const uint32_t lo = static_cast<uint32_t>(act8_code(x0, s, inv)) & 0xFFu;
-      const uint32_t hi = static_cast<uint32_t>(act8_code(x1, s, inv)) & 0xFFu;
-      *reinterpret_cast<uint16_t*>((w == 0 ? a.kept.G8 : a.kept.U8) + at) = static_cast<uint16_t>(lo | (hi << 8));
+      const float s = act8_scale(amax), inv = act8_inverse(s);
+      const float x[4] = {x0, x1, 0.0f, 0.0f};
+      *reinterpret_cast<uint16_t*>((w == 0 ? a.kept.G8 : a.kept.U8) + at) =
+          static_cast<uint16_t>(act8_codes4(x, s, inv));
       if (lane == 0) {
         (w == 0 ? a.kept.Gs : a.kept.Us)[row * (a.N / 64) + n / 64] = s;
         if (!(amax <= FLT_MAX)) raise_status(a.d_status, QLORA_ERR_NONFINITE);

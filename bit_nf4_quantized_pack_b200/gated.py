@@ -16,7 +16,7 @@ import torch
 
 from . import _args
 from ._lib import QLORA_ACT_GELU, QLORA_ACT_SILU, GatedSavedC, check, lib
-from .act8 import Act8, check_act8
+from .act8 import Act8, act8_struct, new_act8
 
 __all__ = ["GatedSaved", "gated_forward", "gated_backward"]
 
@@ -34,31 +34,26 @@ class GatedSaved:
 
     @staticmethod
     def empty(M: int, N: int, r: int, save: str, device="cuda") -> "GatedSaved":
-        def pre():
-            if save == "int8":
-                return Act8.empty(M, N, device)
-            return torch.empty((M, N), dtype=torch.bfloat16, device=device)
-
-        def z():
-            return torch.empty((M, r), dtype=torch.bfloat16, device=device)
-        if save not in ("bf16", "int8"):
-            raise ValueError("save must be 'bf16' or 'int8'")
-        return GatedSaved(pre(), pre(), z(), z())
+        return _new_saved(M, N, r, save, torch.empty(0, dtype=torch.bfloat16, device=device))
 
     def cstruct(self, M, N, r, dev) -> GatedSavedC:
-        _args.tensor(self.Zg, "saved.Zg", (M, r), dev)
-        _args.tensor(self.Zu, "saved.Zu", (M, r), dev)
-        s = GatedSavedC(Zg=self.Zg.data_ptr(), Zu=self.Zu.data_ptr())
+        zg = _args.tensor(self.Zg, "saved.Zg", (M, r), dev)
+        zu = _args.tensor(self.Zu, "saved.Zu", (M, r), dev)
         if isinstance(self.G, Act8):
-            check_act8(self.G, "saved.G", (M, N), dev)
-            check_act8(self.U, "saved.U", (M, N), dev)
-            s.G8, s.G_scales = self.G.codes.data_ptr(), self.G.scales.data_ptr()
-            s.U8, s.U_scales = self.U.codes.data_ptr(), self.U.scales.data_ptr()
-        else:
-            _args.tensor(self.G, "saved.G", (M, N), dev)
-            _args.tensor(self.U, "saved.U", (M, N), dev)
-            s.G, s.U = self.G.data_ptr(), self.U.data_ptr()
-        return s
+            g, u = act8_struct(self.G, "saved.G", M, N, dev), act8_struct(self.U, "saved.U", M, N, dev)
+            return GatedSavedC(None, None, g.codes, u.codes, g.scales, u.scales, zg, zu)
+        return GatedSavedC(_args.tensor(self.G, "saved.G", (M, N), dev), _args.tensor(self.U, "saved.U", (M, N), dev),
+                           None, None, None, None, zg, zu)
+
+
+def _new_saved(M, N, r, save, like):
+    """Buffers for a GatedSaved beside `like` (a bf16 tensor)."""
+    if save == "int8":
+        return GatedSaved(new_act8(M, N, like), new_act8(M, N, like), like.new_empty((M, r)), like.new_empty((M, r)))
+    if save == "bf16":
+        return GatedSaved(like.new_empty((M, N)), like.new_empty((M, N)), like.new_empty((M, r)),
+                          like.new_empty((M, r)))
+    raise ValueError("save must be None, 'bf16' or 'int8'")
 
 
 def _act_code(act):
@@ -68,15 +63,14 @@ def _act_code(act):
 
 
 def _weights(K, dev, wg, wu, Ag, Bg, Au, Bu):
+    """(N, r, the two weights' C structs, the four adapters' addresses)."""
     N = wg.shape[1] if len(wg.shape) == 2 else -1
-    _args.weight(wg, "wg", (K, N), dev)
-    _args.weight(wu, "wu", (K, N), dev)
     if not isinstance(Ag, torch.Tensor) or Ag.dim() != 2:
         raise TypeError("Ag must be a matrix")
     r = Ag.shape[1]
-    for t, name, shape in ((Ag, "Ag", (K, r)), (Bg, "Bg", (r, N)), (Au, "Au", (K, r)), (Bu, "Bu", (r, N))):
-        _args.tensor(t, name, shape, dev)
-    return N, r
+    return (N, r, _args.weight(wg, "wg", K, N, dev), _args.weight(wu, "wu", K, N, dev),
+            (_args.tensor(Ag, "Ag", (K, r), dev), _args.tensor(Bg, "Bg", (r, N), dev),
+             _args.tensor(Au, "Au", (K, r), dev), _args.tensor(Bu, "Bu", (r, N), dev)))
 
 
 def gated_forward(X, wg, wu, Ag, Bg, Au, Bu, c: float, *, act: str = "silu", save: str | None = None,
@@ -91,24 +85,20 @@ def gated_forward(X, wg, wu, Ag, Bg, Au, Bu, c: float, *, act: str = "silu", sav
     from . import _finish, new_status
     M, K, dev = _args.cuda_2d(X, "X")
     code = _act_code(act)
-    N, r = _weights(K, dev, wg, wu, Ag, Bg, Au, Bu)
+    N, r, cg, cu, adapters = _weights(K, dev, wg, wu, Ag, Bg, Au, Bu)
     with _args.on(dev):
-        if H is None:
-            H = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        else:
-            _args.tensor(H, "H", (M, N), dev)
+        H = _args.output(H, X, "H", (M, N))
         if saved is None and save is not None:
-            saved = GatedSaved.empty(M, N, r, save, dev)
+            saved = _new_saved(M, N, r, save, X)
         kept = C.byref(saved.cstruct(M, N, r, dev)) if saved is not None else None
-        need = lib.qlora_gated_fwd_workspace_size(M, K, N, r)
-        ws = _args.workspace(workspace, need, dev)
+        ws = _args.workspace(workspace, lib.qlora_gated_fwd_workspace_size(M, K, N, r), X)
         own = status is None
         status = new_status(dev) if own else status
-        check(lib.qlora_gated_fwd(M, K, N, r, X.data_ptr(), C.byref(wg.cstruct()), C.byref(wu.cstruct()),
-                                  Ag.data_ptr(), Bg.data_ptr(), Au.data_ptr(), Bu.data_ptr(), float(c), code,
+        check(lib.qlora_gated_fwd(M, K, N, r, X.data_ptr(), C.byref(cg), C.byref(cu), *adapters, c, code,
                                   H.data_ptr(), kept, ws.data_ptr(), ws.numel(), status.data_ptr(),
                                   _args.stream(dev)), "qlora_gated_fwd")
-        _finish(status, own, "qlora_gated_fwd")
+        if own:
+            _finish(status, own, "qlora_gated_fwd")
     return H, saved
 
 
@@ -122,35 +112,27 @@ def gated_backward(dH, X, saved: GatedSaved, wg, wu, Ag, Bg, Au, Bu, c: float, *
     code, gcode = _act_code(act), _args.grad_code(grad_dtype)
     is8 = isinstance(X, Act8)
     K = X.shape[1] if (is8 or isinstance(X, torch.Tensor)) and len(X.shape) == 2 else -1
-    if is8:
-        check_act8(X, "X", (M, K), dev)
-    else:
-        _args.tensor(X, "X", (M, K), dev)
-    Nw, r = _weights(K, dev, wg, wu, Ag, Bg, Au, Bu)
+    x8 = act8_struct(X, "X", M, K, dev) if is8 else None
+    x16 = None if is8 else _args.tensor(X, "X", (M, K), dev)
+    Nw, r, cg, cu, adapters = _weights(K, dev, wg, wu, Ag, Bg, Au, Bu)
     if Nw != N:
         raise ValueError(f"dH must have {Nw} columns, not {N}")
     if not isinstance(saved, GatedSaved):
         raise TypeError("saved must be the GatedSaved of the forward")
+    kept = saved.cstruct(M, N, r, dev)
     with _args.on(dev):
-        kept = saved.cstruct(M, N, r, dev)
-        out = []
-        for t, name, shape, dt in ((dX, "dX", (M, K), torch.bfloat16), (dAg, "dAg", (K, r), grad_dtype),
-                                   (dBg, "dBg", (r, N), grad_dtype), (dAu, "dAu", (K, r), grad_dtype),
-                                   (dBu, "dBu", (r, N), grad_dtype)):
-            if t is None:
-                t = torch.empty(shape, dtype=dt, device=dev)
-            else:
-                _args.tensor(t, name, shape, dev, dt)
-            out.append(t)
-        need = lib.qlora_gated_bwd_workspace_size(M, K, N, r)
-        ws = _args.workspace(workspace, need, dev)
+        dX = _args.output(dX, dH, "dX", (M, K))
+        dAg = _args.output(dAg, dH, "dAg", (K, r), grad_dtype)
+        dBg = _args.output(dBg, dH, "dBg", (r, N), grad_dtype)
+        dAu = _args.output(dAu, dH, "dAu", (K, r), grad_dtype)
+        dBu = _args.output(dBu, dH, "dBu", (r, N), grad_dtype)
+        ws = _args.workspace(workspace, lib.qlora_gated_bwd_workspace_size(M, K, N, r), dH)
         own = status is None
         status = new_status(dev) if own else status
-        x8 = C.byref(X.cstruct()) if is8 else None
-        check(lib.qlora_gated_bwd(M, K, N, r, dH.data_ptr(), None if is8 else X.data_ptr(), x8,
-                                  C.byref(kept), C.byref(wg.cstruct()), C.byref(wu.cstruct()),
-                                  Ag.data_ptr(), Bg.data_ptr(), Au.data_ptr(), Bu.data_ptr(), float(c), code,
-                                  *(t.data_ptr() for t in out), gcode, ws.data_ptr(), ws.numel(),
+        check(lib.qlora_gated_bwd(M, K, N, r, dH.data_ptr(), x16, C.byref(x8) if is8 else None, C.byref(kept),
+                                  C.byref(cg), C.byref(cu), *adapters, c, code, dX.data_ptr(), dAg.data_ptr(),
+                                  dBg.data_ptr(), dAu.data_ptr(), dBu.data_ptr(), gcode, ws.data_ptr(), ws.numel(),
                                   status.data_ptr(), _args.stream(dev)), "qlora_gated_bwd")
-        _finish(status, own, "qlora_gated_bwd")
-    return tuple(out)
+        if own:
+            _finish(status, own, "qlora_gated_bwd")
+    return dX, dAg, dBg, dAu, dBu

@@ -19,12 +19,12 @@ __all__ = ["head_loss_forward", "head_loss_backward"]
 def _head(X, w, labels, vocab):
     M, K, dev = _args.cuda_2d(X, "X")
     N = w.shape[1] if len(w.shape) == 2 else -1
-    _args.weight(w, "w", (K, N), dev)
-    _args.tensor(labels, "labels", (M,), dev, torch.int64)
+    st = _args.weight(w, "w", K, N, dev)
+    y = _args.tensor(labels, "labels", (M,), dev, torch.int64)
     vocab = N if vocab is None else int(vocab)
     if not 1 <= vocab <= N:
         raise ValueError(f"vocab must be 1 .. {N}, not {vocab}")
-    return M, K, N, vocab, dev
+    return M, K, N, vocab, dev, st, y
 
 
 def head_loss_forward(X, w, labels, *, vocab: int | None = None, ignore_index: int = -100, loss=None,
@@ -35,24 +35,19 @@ def head_loss_forward(X, w, labels, *, vocab: int | None = None, ignore_index: i
     N by default) are padding.  Rows whose label is ``ignore_index`` have loss
     0; any other label outside 0 .. vocab - 1 is a device error."""
     from . import _finish, new_status
-    M, K, N, vocab, dev = _head(X, w, labels, vocab)
+    M, K, N, vocab, dev, st, y = _head(X, w, labels, vocab)
     with _args.on(dev):
-        out = []
-        for t, name in ((loss, "loss"), (lse, "lse")):
-            if t is None:
-                t = torch.empty((M,), dtype=torch.float32, device=dev)
-            else:
-                _args.tensor(t, name, (M,), dev, torch.float32)
-            out.append(t)
-        need = lib.qlora_head_loss_fwd_workspace_size(M, K, N)
-        ws = _args.workspace(workspace, need, dev)
+        loss = _args.output(loss, X, "loss", (M,), torch.float32)
+        lse = _args.output(lse, X, "lse", (M,), torch.float32)
+        ws = _args.workspace(workspace, lib.qlora_head_loss_fwd_workspace_size(M, K, N), X)
         own = status is None
         status = new_status(dev) if own else status
-        check(lib.qlora_head_loss_fwd(M, K, N, vocab, X.data_ptr(), C.byref(w.cstruct()), labels.data_ptr(),
-                                      int(ignore_index), out[0].data_ptr(), out[1].data_ptr(), ws.data_ptr(),
-                                      ws.numel(), status.data_ptr(), _args.stream(dev)), "qlora_head_loss_fwd")
-        _finish(status, own, "qlora_head_loss_fwd")
-    return tuple(out)
+        check(lib.qlora_head_loss_fwd(M, K, N, vocab, X.data_ptr(), C.byref(st), y, int(ignore_index),
+                                      loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(),
+                                      status.data_ptr(), _args.stream(dev)), "qlora_head_loss_fwd")
+        if own:
+            _finish(status, own, "qlora_head_loss_fwd")
+    return loss, lse
 
 
 def head_loss_backward(dloss, X, lse, w, labels, *, vocab: int | None = None, ignore_index: int = -100,
@@ -60,21 +55,17 @@ def head_loss_backward(dloss, X, lse, w, labels, *, vocab: int | None = None, ig
     """dX (bf16 M x K) from dloss (fp32 M, the gradient of each row's loss: 1/count
     for the mean over count labels) and the forward's lse."""
     from . import _finish, new_status
-    M, K, N, vocab, dev = _head(X, w, labels, vocab)
-    _args.tensor(dloss, "dloss", (M,), dev, torch.float32)
-    _args.tensor(lse, "lse", (M,), dev, torch.float32)
+    M, K, N, vocab, dev, st, y = _head(X, w, labels, vocab)
+    dl = _args.tensor(dloss, "dloss", (M,), dev, torch.float32)
+    ls = _args.tensor(lse, "lse", (M,), dev, torch.float32)
     with _args.on(dev):
-        if dX is None:
-            dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-        else:
-            _args.tensor(dX, "dX", (M, K), dev)
-        need = lib.qlora_head_loss_bwd_workspace_size(M, K, N)
-        ws = _args.workspace(workspace, need, dev)
+        dX = _args.output(dX, X, "dX", (M, K))
+        ws = _args.workspace(workspace, lib.qlora_head_loss_bwd_workspace_size(M, K, N), X)
         own = status is None
         status = new_status(dev) if own else status
-        check(lib.qlora_head_loss_bwd(M, K, N, vocab, dloss.data_ptr(), X.data_ptr(), lse.data_ptr(),
-                                      C.byref(w.cstruct()), labels.data_ptr(), int(ignore_index),
+        check(lib.qlora_head_loss_bwd(M, K, N, vocab, dl, X.data_ptr(), ls, C.byref(st), y, int(ignore_index),
                                       dX.data_ptr(), ws.data_ptr(), ws.numel(), status.data_ptr(),
                                       _args.stream(dev)), "qlora_head_loss_bwd")
-        _finish(status, own, "qlora_head_loss_bwd")
+        if own:
+            _finish(status, own, "qlora_head_loss_bwd")
     return dX
