@@ -1,15 +1,25 @@
-"""A chain of frozen-NF4 + LoRA linear layers with a saved-activation policy.
+"""A chain of frozen-NF4 + LoRA layers with a saved-activation policy, and the
+loss behind it.
 
-Y_0 = X, Y_i = Y_{i-1} Ŵ_i + c_i (Y_{i-1} A_i) B_i, as in a stack of a decoder
-layer's projections (the nonlinear parts of a real layer between them are not
-part of this library).  The backward walks the layers in reverse; each layer's
-input Y_{i-1} is kept, and its rank-r product Zc_i is either kept
-(``policy="save"``) or recomputed inside the backward call
-(``policy="recompute"``: M·r bf16 less per layer between the passes, at the
-price of one rank-r contraction per layer; the page "SFT（四）：QLoRA的4-bit量化
-与LoRA微调原理", §26.2 为什么开启 Gradient Checkpointing, states the same trade of
-recomputation for stored activations).  Both policies give identical bits:
-the recomputation uses the forward's kernel and split.
+A layer is a linear (``Layer``: Y_i = Y_{i-1} Ŵ_i + c_i (Y_{i-1} A_i) B_i) or a
+gated block over two weights (``GatedLayer``: gate and up projections,
+activation and product), as in a stack of a decoder layer's projections (its
+attention and norms are not part of this library).  The backward walks the
+layers in reverse.  What a layer keeps between the passes is the policy's:
+
+    "save"       its input, and its rank-r products (a gated block: also g and u) in bf16
+    "recompute"  its input alone; the backward forms the rest again, to the same bits
+    "int8"       its input (a gated block: also g and u) as 8-bit checkpoints,
+                 and its rank-r products in bf16
+
+"recompute" keeps M·r bf16 less per linear, and 4·M·N bytes less per gated
+block, at the price of a rank-r contraction, or the block's forward (the page
+"SFT（四）：QLoRA的4-bit量化与LoRA微调原理", §26.2 为什么开启 Gradient Checkpointing,
+states this trade); "int8" keeps 1.0625 bytes an element where "save" keeps 2,
+and its gradients of A carry the checkpoint's rounding.
+
+``HeadLoss`` is the softmax cross entropy behind an NF4 head;
+``LinearChain.loss_backward`` runs a whole training step's passes through it.
 """
 from __future__ import annotations
 
@@ -17,10 +27,13 @@ from dataclasses import dataclass
 
 import torch
 
-from . import linear_backward, linear_forward, new_status, status_sync
+from . import (act8_quantize, gated_backward, gated_forward, head_loss_backward, head_loss_forward,
+               linear_backward, linear_forward, new_status, status_sync)
 from ._lib import QLoRAError
 
-__all__ = ["Layer", "LinearChain"]
+__all__ = ["Layer", "GatedLayer", "HeadLoss", "LinearChain"]
+
+POLICIES = ("save", "recompute", "int8")
 
 
 @dataclass
@@ -30,16 +43,64 @@ class Layer:
     B: torch.Tensor    # r x N_i bf16
     c: float
 
+    @property
+    def widths(self):
+        return self.w.shape
+
+
+@dataclass
+class GatedLayer:
+    """act(Y Ŵg + c (Y Ag) Bg) · (Y Ŵu + c (Y Au) Bu)."""
+    wg: object         # NF4Weights of the K_i x N_i gate and up projections
+    wu: object
+    Ag: torch.Tensor   # K_i x r bf16
+    Bg: torch.Tensor   # r x N_i bf16
+    Au: torch.Tensor
+    Bu: torch.Tensor
+    c: float
+    act: str = "silu"
+
+    @property
+    def widths(self):
+        return self.wg.shape
+
+    def args(self):
+        return self.wg, self.wu, self.Ag, self.Bg, self.Au, self.Bu, self.c
+
+
+@dataclass
+class HeadLoss:
+    """Mean softmax cross entropy over the labels that are not ignore_index."""
+    w: object                    # NF4Weight of the K x N head
+    vocab: int | None = None     # columns that count (all N)
+    ignore_index: int = -100
+
+    def forward(self, X, labels, status=None):
+        """Returns (mean loss, row losses, lse), all on the device."""
+        loss, lse = head_loss_forward(X, self.w, labels, vocab=self.vocab, ignore_index=self.ignore_index,
+                                      status=status)
+        return loss.sum() / (labels != self.ignore_index).sum().clamp(min=1), loss, lse
+
+    def backward(self, X, lse, labels, status=None):
+        """dX of the mean loss."""
+        counted = labels != self.ignore_index
+        dloss = counted.to(torch.float32) / counted.sum().clamp(min=1)
+        return head_loss_backward(dloss, X, lse, self.w, labels, vocab=self.vocab,
+                                  ignore_index=self.ignore_index, status=status)
+
 
 class LinearChain:
-    def __init__(self, layers, policy: str = "save"):
-        if policy not in ("save", "recompute"):
-            raise ValueError("policy must be 'save' or 'recompute'")
+    def __init__(self, layers, policy: str = "save", head: HeadLoss | None = None):
+        if policy not in POLICIES:
+            raise ValueError("policy must be 'save', 'recompute' or 'int8'")
         for a, b in zip(layers, layers[1:]):
-            if a.w.shape[1] != b.w.shape[0]:
+            if a.widths[1] != b.widths[0]:
                 raise ValueError("layer widths do not chain")
+        if head is not None and layers and layers[-1].widths[1] != head.w.shape[0]:
+            raise ValueError("the head's width does not chain")
         self.layers = list(layers)
         self.policy = policy
+        self.head = head
         self._inputs = []
         self._zc = []
 
@@ -49,15 +110,20 @@ class LinearChain:
         self._inputs, self._zc = [], []
         h = X
         for L in self.layers:
-            self._inputs.append(h)
-            h, zc = linear_forward(h, L.w, L.A, L.B, L.c, status=status)
-            self._zc.append(zc if self.policy == "save" else None)
+            self._inputs.append(act8_quantize(h, status=status) if self.policy == "int8" else h)
+            if isinstance(L, GatedLayer):
+                save = {"save": "bf16", "int8": "int8", "recompute": None}[self.policy]
+                h, kept = gated_forward(h, *L.args(), act=L.act, save=save, status=status)
+            else:
+                h, kept = linear_forward(h, L.w, L.A, L.B, L.c, status=status)
+            self._zc.append(None if self.policy == "recompute" else kept)
         if own:
             self._check(status, "forward")
         return h
 
     def backward(self, dY: torch.Tensor, status: torch.Tensor | None = None):
-        """Returns (dX, [(dA_i, dB_i) for each layer])."""
+        """Returns (dX, [the layers' adapter gradients]): (dA_i, dB_i) of a
+        linear, (dAg_i, dBg_i, dAu_i, dBu_i) of a gated block."""
         if not self._inputs:
             raise RuntimeError("backward before forward")
         own = status is None
@@ -65,16 +131,34 @@ class LinearChain:
         grads = [None] * len(self.layers)
         g = dY
         for i in reversed(range(len(self.layers))):
-            L = self.layers[i]
-            g, dA, dB = linear_backward(g, self._inputs[i], self._zc[i], L.w, L.A, L.B, L.c,
-                                        status=status)
-            grads[i] = (dA, dB)
+            L, x, kept = self.layers[i], self._inputs[i], self._zc[i]
+            if isinstance(L, GatedLayer):
+                if kept is None:
+                    _, kept = gated_forward(x, *L.args(), act=L.act, save="bf16", status=status)
+                g, *d = gated_backward(g, x, kept, *L.args(), act=L.act, status=status)
+            else:
+                g, *d = linear_backward(g, x, kept, L.w, L.A, L.B, L.c, status=status)
+            grads[i] = tuple(d)
         if own:
             self._check(status, "backward")
         return g, grads
 
+    def loss_backward(self, X: torch.Tensor, labels: torch.Tensor, status: torch.Tensor | None = None):
+        """The chain, its head's mean loss over `labels` (int64, one a row) and
+        the backward through both.  Returns (mean loss, dX, adapter gradients)."""
+        if self.head is None:
+            raise RuntimeError("the chain has no head")
+        own = status is None
+        status = new_status(X.device) if own else status
+        h = self.forward(X, status)
+        mean, _, lse = self.head.forward(h, labels, status)
+        dX, grads = self.backward(self.head.backward(h, lse, labels, status), status)
+        if own:
+            self._check(status, "loss_backward")
+        return mean, dX, grads
+
     @staticmethod
     def _check(status, where):
-        code, mask = status_sync(status)
+        code, _ = status_sync(status)
         if code != 0:
-            raise QLoRAError(f"LinearChain.{where}: device status {code} (mask {mask})")
+            raise QLoRAError(code, f"LinearChain.{where}")
