@@ -27,6 +27,7 @@ import torch
 
 from . import _args, _lib
 from ._lib import NF4StateC, QLoRAError, check, lib
+from ._status import _finish, new_status, status_clear, status_sync
 from .act8 import Act8, act8_dequantize, act8_quantize, act8_struct
 from .gated import GatedSaved, gated_backward, gated_forward
 from .loss import head_loss_backward, head_loss_forward
@@ -113,21 +114,6 @@ class NF4Weight:
         return w
 
 
-def new_status(device="cuda") -> torch.Tensor:
-    return torch.zeros(1, dtype=torch.int32, device=device)
-
-
-def status_sync(status: torch.Tensor):
-    """(first error code or 0, raw bit mask); synchronizes the current stream."""
-    mask = C.c_int32(0)
-    code = lib.qlora_status_sync(_ptr(status), _stream(), C.byref(mask))
-    return int(code), int(mask.value)
-
-
-def status_clear(status: torch.Tensor) -> None:
-    check(lib.qlora_status_clear(_ptr(status), _stream()), "qlora_status_clear")
-
-
 class _WorkspaceCache:
     """Reuses one device buffer per (purpose, device, current stream) so
     repeated calls do not allocate; grows when a larger workspace is needed.
@@ -173,12 +159,6 @@ class _WorkspaceCache:
 
 
 _ws = _WorkspaceCache()
-
-
-def _finish(status, own_status, where):
-    if own_status:
-        code, _ = status_sync(status)
-        check(code, where)
 
 
 def quantize(W: torch.Tensor, double_quant: bool = True, *, out: NF4Weight | None = None,

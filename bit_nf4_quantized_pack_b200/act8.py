@@ -15,6 +15,7 @@ import torch
 
 from . import _args
 from ._lib import Act8C, check, lib
+from ._status import _finish, new_status
 
 __all__ = ["Act8", "act8_quantize", "act8_dequantize"]
 
@@ -47,24 +48,26 @@ def act8_struct(a, name, M, K, dev):
     """The C struct of an Act8 of M x K on `dev` with buffers of the right extents."""
     if not isinstance(a, Act8):
         raise TypeError(f"{name} must be an Act8")
-    return Act8C(M, K, _args.tensor(a.codes, f"{name}.codes", (M, K), dev, torch.int8),
-                 _args.tensor(a.scales, f"{name}.scales", (M, K // 64), dev, torch.float32))
+    return Act8C(M, K, _args.tensor(a.codes, name, (M, K), dev, torch.int8),
+                 _args.tensor(a.scales, name, (M, K // 64), dev, torch.float32))
 
 
 def new_act8(M, K, like):
-    """Buffers for an Act8 of M x K beside `like`."""
-    return Act8(like.new_empty((M, K), dtype=torch.int8), like.new_empty((M, K // 64), dtype=torch.float32))
+    """A new Act8 of M x K beside `like`, and its C struct."""
+    codes = like.new_empty((M, K), dtype=torch.int8)
+    scales = like.new_empty((M, K // 64), dtype=torch.float32)
+    return Act8(codes, scales), Act8C(M, K, codes.data_ptr(), scales.data_ptr())
 
 
 def act8_quantize(X: torch.Tensor, *, out: Act8 | None = None, status: torch.Tensor | None = None) -> Act8:
     """The 8-bit checkpoint of a contiguous CUDA bf16 matrix whose row length
     is a multiple of 64.  A NaN or infinity in X is a device error."""
-    from . import _finish, new_status
     M, K, dev = _args.cuda_2d(X, "X")
     with _args.on(dev):
         if out is None:
-            out = new_act8(M, K, X)
-        st = act8_struct(out, "out", M, K, dev)
+            out, st = new_act8(M, K, X)
+        else:
+            st = act8_struct(out, "out", M, K, dev)
         own = status is None
         status = new_status(dev) if own else status
         check(lib.qlora_act8_quantize(X.data_ptr(), C.byref(st), status.data_ptr(), _args.stream(dev)),

@@ -101,7 +101,15 @@ __device__ __forceinline__ uint32_t act8_codes4(const float (&x)[4], float s, fl
   return act8_pack(r[0], r[1], r[2], r[3]);
 }
 
-// The code's value before its rounding to bf16.
-__device__ __forceinline__ float act8_value(int8_t q, float s) { return static_cast<float>(q) * s; }
+// The values of four codes before their rounding to bf16, fl32(code * s).  A code
+// becomes a float through the mantissa (2^23 + 128 + code, less 2^23 + 128: both
+// exact), since the conversion instruction runs at a quarter of the rate.
+__device__ __forceinline__ void act8_values4(uint32_t codes, float s, float (&v)[4]) {
+  const uint32_t u = codes ^ 0x80808080u;
+  v[0] = __fmul_rn(__fadd_rn(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540)), -8388736.0f), s);
+  v[1] = __fmul_rn(__fadd_rn(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7541)), -8388736.0f), s);
+  v[2] = __fmul_rn(__fadd_rn(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7542)), -8388736.0f), s);
+  v[3] = __fmul_rn(__fadd_rn(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7543)), -8388736.0f), s);
+}
 
 }  // namespace qnf4

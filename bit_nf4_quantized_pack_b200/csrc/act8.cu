@@ -86,13 +86,11 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t i = i0 + u * stride;
-      const uint32_t w[2] = {q[u].x, q[u].y};
-      uint32_t o[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t b = w[k >> 1] >> (16 * (k & 1));
-        o[k] = pack_bf16x2(act8_value(static_cast<int8_t>(b), s[u]), act8_value(static_cast<int8_t>(b >> 8), s[u]));
-      }
+      float v[4], w[4];
+      act8_values4(q[u].x, s[u], v);
+      act8_values4(q[u].y, s[u], w);
+      const uint32_t o[4] = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(w[0], w[1]),
+                             pack_bf16x2(w[2], w[3])};
       if (i < pieces) X[i] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }

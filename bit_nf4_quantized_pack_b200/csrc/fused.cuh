@@ -25,8 +25,8 @@ __constant__ float kNF4g[32] = {QNF4_TABLE_VALUES, QNF4_INT4_VALUES};
 //   kModeGatedBwd   dX = dG·Ŵgᵀ + dU·Ŵuᵀ + dZg·Agᵀ + dZu·Auᵀ
 //   kModeLossStats  the maximum and sum of exponentials of each row of X·Ŵ over
 //                   256 columns, and the label's logit
-//   kModeLossGrad   bf16 of dloss·(softmax(X·Ŵ) - onehot) over a piece of columns
-//   kModeLossDX     dX (+)= P·Ŵᵀ over a piece of columns
+//   kModeLossGrad   P = bf16(softmax(X·Ŵ) - onehot) over a piece of columns
+//   kModeLossDX     dX (+)= dloss·(P·Ŵᵀ) over a piece of columns
 // "forward" and "backward" below are the operand layouts: the modes with Ŵᵀ
 // (Bwd, GatedBwd, LossDX) use the backward one.
 //
@@ -166,7 +166,7 @@ struct LossArgs : SplitArgs {
   const int64_t* labels;
   int64_t ignore_index;
   const float* lse;     // LossGrad
-  const float* dloss;   // LossGrad
+  const float* dloss;   // LossDX
   float2* stats;        // LossStats: [n_tiles][M] (maximum, sum of exponentials)
   float* label_logit;   // LossStats: [M]
   float* acc;           // LossDX: fp32 [M][Nout] sums over the pieces
@@ -493,14 +493,22 @@ __device__ __forceinline__ void epilogue_loss_stats(const LossArgs& a, uint32_t 
   if (in) a.stats[static_cast<int64_t>(n0 / kFAccCols) * a.M + row] = make_float2(m, s);
 }
 
-// P = dloss (exp(l - lse) - onehot(label)) of this lane's row, bf16; zero in
-// the columns from `vocab` on and in rows whose label does not count.
+// Whether a row's label counts.
+__device__ __forceinline__ bool label_counts(const LossArgs& a, int row) {
+  if (row >= a.M) return false;
+  const int64_t label = a.labels[row];
+  return label != a.ignore_index && label >= 0 && label < a.vocab;
+}
+
+// P = exp(l - lse) - onehot(label) of this lane's row, bf16; zero in the
+// columns from `vocab` on and in rows whose label does not count.  dloss comes
+// in behind the product with Ŵᵀ: in P it would be rounded with it, and alike in
+// every row of a mean (-dloss at the label where the token was not expected).
 __device__ __forceinline__ void epilogue_loss_grad(const LossArgs& a, uint32_t tbase, int row, int n0) {
   const bool in = row < a.M;
   const int64_t label = in ? a.labels[row] : -1;
-  const bool counts = in && label != a.ignore_index && label >= 0 && label < a.vocab;
+  const bool counts = label_counts(a, row);
   const float lse = in ? a.lse[row] : 0.0f;
-  const float d = counts ? a.dloss[row] : 0.0f;
 #pragma unroll 1
   for (int c = 0; c < kFAccCols / 32; ++c) {
     if (n0 + c * 32 >= a.Nout) break;   // the same for the whole warp
@@ -516,39 +524,51 @@ __device__ __forceinline__ void epilogue_loss_grad(const LossArgs& a, uint32_t t
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         const float e = ex2((__uint_as_float(v[i]) - lse) * kLog2E);
-        p[i] = counts && i < nv ? d * (e - (i == at ? 1.0f : 0.0f)) : 0.0f;
+        p[i] = counts && i < nv ? e - (i == at ? 1.0f : 0.0f) : 0.0f;
       }
       store_bf16x32(a.out + static_cast<int64_t>(row) * a.Nout + n0 + c * 32, p);
     }
   }
 }
 
-// dX of one output column (this lane) over 32 rows, added to the pieces
-// before this one in fp32 (without a result, so that no load waits between
-// stores); the last piece adds the sums and rounds to bf16.
-__device__ __forceinline__ void epilogue_loss_dx(const LossArgs& a, const uint32_t (&v)[32], int col, int row0) {
-  if (col >= a.Nout || row0 >= a.M) return;
+// dX of one output column (this lane) over 32 rows: times the row's dloss (0
+// where the label does not count), added to the pieces before this one in fp32
+// (without a result, so that no load waits between stores); the last piece
+// adds the sums and rounds to bf16.  `scale` is dloss of row row0 + lane.
+__device__ __forceinline__ void epilogue_loss_dx(const LossArgs& a, const uint32_t (&v)[32], float scale, int split,
+                                                 int col, int row0) {
   const int64_t ld = a.Nout;
   const int64_t at = row0 * ld + col;
-  const int nrows = a.M - row0;
+  const int nrows = col < a.Nout ? a.M - row0 : 0;
+  float x[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]) * __shfl_sync(0xFFFFFFFFu, scale, i);
+  if (a.splits > 1) {
+    float* dst = a.part + static_cast<int64_t>(split) * a.M * ld + at;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < nrows) dst[i * ld] = x[i];
+    return;
+  }
   if (!a.last) {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
       if (i < nrows) {
         if (a.first)
-          a.acc[at + i * ld] = __uint_as_float(v[i]);
+          a.acc[at + i * ld] = x[i];
         else
-          atomicAdd(a.acc + at + i * ld, __uint_as_float(v[i]));   // one thread per element: no order
+          atomicAdd(a.acc + at + i * ld, x[i]);   // one thread per element: no order
       }
     return;
   }
-  float old[32];
+  if (!a.first) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) old[i] = !a.first && i < nrows ? a.acc[at + i * ld] : 0.0f;
+    for (int i = 0; i < 32; ++i)
+      if (i < nrows) x[i] += a.acc[at + i * ld];
+  }
 #pragma unroll
   for (int i = 0; i < 32; ++i)
-    if (i < nrows)
-      a.out[at + i * ld] = static_cast<uint16_t>(pack_bf16x2(__uint_as_float(v[i]) + old[i], 0.0f));
+    if (i < nrows) a.out[at + i * ld] = static_cast<uint16_t>(pack_bf16x2(x[i], 0.0f));
 }
 
 // A split item's fp32 sums of one output column over 32 rows; false where the
@@ -964,6 +984,15 @@ __global__ void __launch_bounds__(kFThreads, 1)
       const int m0 = (tile % args.m_tiles) * kFPairRows;
       const int n0 = (tile / args.m_tiles) * kTileCols;
       const int nh = tile_slices<kMode>(args.M, m0);
+      // loss: dloss of the lane's row in the next 32 (0 where its label does not
+      // count), loaded 32 rows ahead
+      auto row_scale = [&](int row) -> float {
+        if constexpr (kMode == kModeLossDX) {
+          if (label_counts(args, row)) return args.dloss[row];
+        }
+        return 0.0f;
+      };
+      float next_scale = row_scale(m0 + lane);
       if (*abort_flag || !mbar_wait(tfull, tc & 1)) { ok = false; break; }
       tc_fence_after();
       const int64_t ld = args.Nout;
@@ -985,10 +1014,13 @@ __global__ void __launch_bounds__(kFThreads, 1)
           uint32_t v[32];
           tmem_ld_32x32b_x32(tbase + c * 32, v);
           tmem_ld_wait();
-          if (mode_splits(kMode) && split_sums(args, v, split, n0 + 128 * rank + q * 32 + lane,
-                                               m0 + h * kFAccCols + c * 32)) {
-          } else if constexpr (kMode == kModeLossDX) {
-            epilogue_loss_dx(args, v, n0 + 128 * rank + q * 32 + lane, m0 + h * kFAccCols + c * 32);
+          if constexpr (kMode == kModeLossDX) {
+            const int row0 = m0 + h * kFAccCols + c * 32;
+            const float scale = next_scale;
+            next_scale = row_scale(row0 + 32 + lane);
+            epilogue_loss_dx(args, v, scale, split, n0 + 128 * rank + q * 32 + lane, row0);
+          } else if (kMode == kModeGatedBwd && split_sums(args, v, split, n0 + 128 * rank + q * 32 + lane,
+                                                          m0 + h * kFAccCols + c * 32)) {
           } else if (!kBwd) {
             // lane = output row, 32 consecutive output columns
             const int row = m0 + 256 * rank + h * 128 + q * 32 + lane;

@@ -298,33 +298,34 @@ cudaError_t launch_linear_bwd(int64_t M, int64_t K, int64_t N, int r, const uint
   // dA, dB on the SMs dX leaves free when they can stream their 2 x M x
   // (K + N) bytes there well within dX, else split-K
   const int dx_tiles = fa.m_tiles * fa.n_tiles;
-  // (fp32 gradients of a bf16 input; the split kernel has the other forms)
-  const int dadb_ctas =
-      X8 == nullptr && !grad_bf16 ? rank_rows_ctas(2.0 * M * (K + N), dx_tiles, 5.0) : 0;
+  const int dadb_ctas = rank_rows_ctas(2.0 * M * (K + N), dx_tiles, 5.0);
+  const int modeA = grad_bf16 ? 0 : 1, modeB = grad_bf16 ? 3 : 2;
   if (e == cudaSuccess && X8 != nullptr) {
     SkinnyArgs sa{};
     sa.Mp = static_cast<int>(K);
     sa.ncols = sa.nout = sa.ld = r;
     sa.scale = 1.0f;
-    sa.mode = grad_bf16 ? 0 : 1;
+    sa.mode = modeA;
     sa.out = dA;
     sa.d_status = d_status;
-    e = launch_skinny<true, true, false, true>(
-        SkinnyMaps<false, true>{tdZ}, sa, static_cast<int>(M), Sa, SkinnySecond{},
-        SkinnyA8{X8, X8_scales, static_cast<int>(M), static_cast<int>(K)}, s2);
+    const SkinnyA8 a8{X8, X8_scales, static_cast<int>(M), static_cast<int>(K)};
+    const SkinnyMaps<false, true> maps{tdZ};
+    e = dadb_ctas > 0 ? launch_rank_rows<true, true, true>(maps, sa, static_cast<int>(M), dadb_ctas, a8, s2)
+                      : launch_skinny<true, true, false, true>(maps, sa, static_cast<int>(M), Sa,
+                                                               SkinnySecond{}, a8, s2);
   } else if (e == cudaSuccess) {
     e = dadb_ctas > 0
-            ? run_rank_rows<true, true>(tXmn, tdZ, static_cast<int>(K), static_cast<int>(M), r, 1.0f, 1,
+            ? run_rank_rows<true, true>(tXmn, tdZ, static_cast<int>(K), static_cast<int>(M), r, 1.0f, modeA,
                                         dA, r, dadb_ctas, d_status, s2)
-            : run_skinny<true, true>(tXmn, tdZ, static_cast<int>(K), static_cast<int>(M), r, 1.0f,
-                                     grad_bf16 ? 0 : 1, dA, r, Sa, d_status, s2);
+            : run_skinny<true, true>(tXmn, tdZ, static_cast<int>(K), static_cast<int>(M), r, 1.0f, modeA, dA,
+                                     r, Sa, d_status, s2);
   }
   if (e == cudaSuccess)
     e = dadb_ctas > 0
             ? run_rank_rows<true, true>(tGmn, tZcmn, static_cast<int>(N), static_cast<int>(M), r, 1.0f,
-                                        2, dB, r, dadb_ctas, d_status, s2)
-            : run_skinny<true, true>(tGmn, tZcmn, static_cast<int>(N), static_cast<int>(M), r, 1.0f,
-                                     grad_bf16 ? 3 : 2, dB, r, Sb, d_status, s2);
+                                        modeB, dB, r, dadb_ctas, d_status, s2)
+            : run_skinny<true, true>(tGmn, tZcmn, static_cast<int>(N), static_cast<int>(M), r, 1.0f, modeB,
+                                     dB, r, Sb, d_status, s2);
   if (s2 != st) {
     // always join, so that nothing on st can run ahead of work already queued
     const cudaError_t ej = cudaEventRecord(ss->join, s2);

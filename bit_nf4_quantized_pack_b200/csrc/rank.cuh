@@ -37,7 +37,7 @@ struct SkinnyArgs {
   int nout;          // columns written to `out` (<= ncols)
   float scale;
   int mode;          // 0: bf16 out[Mp][ld]; 1: fp32 out[Mp][ld]; 2: fp32 out[nout][Mp];
-                     // 3: bf16 out[nout][Mp] (the split kernel only)
+                     // 3: bf16 out[nout][Mp]
   void* out;
   int ld;
   uint16_t* out2;    // mode 0 only, may be null: all ncols columns again, bf16 [Mp][ld2]
@@ -77,15 +77,105 @@ struct SkinnyMaps<true, true> {
   CUtensorMap b, b2;
 };
 
-constexpr int kSkA8Warps = 4;   // decoder warps of the 8-bit A operand
+constexpr int kSkA8Group = 4 * kSkW;   // decoder warps of a stage of the 8-bit A operand
+constexpr int kSkA8Turns = 2;          // groups of them that take stages in turn
+constexpr int kSkA8Warps = kSkA8Group * kSkA8Turns;
+constexpr int kSkA8Ahead = 2;          // of its stages, whose codes a decoder thread has in flight
 
 constexpr int kSkRedLd = 65;   // fp32 words per row of the split-sum buffer (bank spread)
 constexpr int kSkMaxSplits = 8;  // portable cluster size
 
-// kA8: A is an MN-major 8-bit checkpoint.  Four more warps (after the
+// One of the 256 decoder threads of an MN-major 8-bit A operand's stage.  Eight
+// warps share its 256 rows (two boxes of two 64-column halves of 64 k' rows): warp w
+// has box w >> 2, half (w >> 1) & 1 and 32 rows of it, a thread 16 codes of four
+// rows eight apart, so that four lanes read a row's 64 bytes together (a lane
+// to a row costs the L1 four times as many passes) and a store phase's eight
+// lanes meet all banks.
+struct A8Decoder {
+  const SkinnyA8& a8;
+  int box, hh, kr, c, col;
+  int64_t bpr;
+
+  struct Rows {
+    uint4 p[4];
+    float s[4];
+  };
+
+  __device__ __forceinline__ A8Decoder(const SkinnyA8& a, int t, int m0)
+      : a8(a), box(t >> 7), hh((t >> 6) & 1), kr(((t >> 5) & 1) * 32 + ((t & 31) >> 2)), c(t & 3),
+        col(m0 + ((t >> 6) & 1) * 64), bpr(a.cols / 64) {}
+
+  // the codes of k' block kb (zeros from block `end` on and past the matrix)
+  __device__ __forceinline__ void fetch(Rows& r, int kb, int end) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = static_cast<int64_t>((kb * kSkW + box) * 64) + kr + 8 * i;
+      r.s[i] = 0.0f;
+      r.p[i] = make_uint4(0, 0, 0, 0);
+      if (kb < end && row < a8.rows && col < a8.cols) {
+        // volatile asm: the loads issue here, stages before their use
+        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.p[i].x), "=r"(r.p[i].y), "=r"(r.p[i].z), "=r"(r.p[i].w)
+                     : "l"(a8.codes + row * a8.cols + col + 16 * c));
+        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(r.s[i]) : "l"(a8.scales + row * bpr + col / 64));
+      }
+    }
+  }
+
+  // their values into the stage, in the 128-byte swizzle of a box
+  __device__ __forceinline__ void store(const Rows& r, uint8_t* stage) const {
+    const uint32_t rowp = smem_u32(stage) + box * 16384 + hh * 8192 + kr * 128;
+    const uint32_t sw = static_cast<uint32_t>(kr & 7) << 4;   // kr + 8 i: the same swizzle
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t q[4] = {r.p[i].x, r.p[i].y, r.p[i].z, r.p[i].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v[4];
+        act8_values4(q[j], r.s[i], v);
+        o[2 * j] = pack_bf16x2(v[0], v[1]);
+        o[2 * j + 1] = pack_bf16x2(v[2], v[3]);
+      }
+      const uint32_t at = rowp + i * 1024;
+      sts128(at + ((c << 5) ^ sw), make_uint4(o[0], o[1], o[2], o[3]));
+      sts128(at + (((c << 5) | 16) ^ sw), make_uint4(o[4], o[5], o[6], o[7]));
+    }
+  }
+
+  // This turn's K blocks of a tile's kb0 .. kb1 - 1, the first of them the
+  // ring's stage use g0.
+  template <typename Wait>
+  __device__ __forceinline__ bool run(int kb0, int kb1, int g0, int turn, uint8_t* sA, uint64_t* full, int lane,
+                                      Wait&& wait_empty) const {
+    Rows r[kSkA8Ahead];
+    const int first = kb0 + ((turn - g0) & (kSkA8Turns - 1));   // stage uses turn, turn + 2, ... are this turn's
+#pragma unroll
+    for (int i = 0; i < kSkA8Ahead; ++i) fetch(r[i], first + i * kSkA8Turns, kb1);
+    for (int kb = first; kb < kb1; kb += kSkA8Ahead * kSkA8Turns) {
+#pragma unroll
+      for (int i = 0; i < kSkA8Ahead; ++i) {
+        const int k = kb + i * kSkA8Turns;
+        if (k < kb1) {
+          const int g = g0 + k - kb0, s = g % kSkStages;
+          if (!wait_empty(g)) return false;
+          store(r[i], sA + s * kSkA);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+          fetch(r[i], k + kSkA8Ahead * kSkA8Turns, kb1);
+        }
+      }
+    }
+    return true;
+  }
+};
+
+// kA8: A is an MN-major 8-bit checkpoint.  Sixteen more warps (after the
 // epilogue's) decode it instead of TMA: a tile row is 64 codes of one k' row
 // and one scale, written as 64 bf16 in the 128-byte swizzle that the box would
-// have; each thread owns two rows of a stage and loads them one stage ahead.
+// have; two groups of eight take stages in turn (one alone spent 2.2 thousand
+// clocks a stage, 40 % of them issuing) and load four stages ahead.
 template <bool kAmn, bool kBmn, bool kPair = false, bool kA8 = false>
 __global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
     skinny_gemm_kernel(const __grid_constant__ SkinnyMaps<kPair, kA8> maps, SkinnyArgs args,
@@ -122,7 +212,7 @@ __global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSkStages; ++s) {
-      mbar_init(&full[s], kA8 ? 1 + kSkA8Warps : 1);
+      mbar_init(&full[s], kA8 ? 1 + kSkA8Group : 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
@@ -195,58 +285,12 @@ __global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
     if (!ok) *abort_flag = 1;
     umma_commit(done);  // also drains whatever was issued
   } else if (kA8 && warp >= 6) {
-    // Decoders of the 8-bit operand.  Row t of a stage's box w (t < 128): half
-    // t >> 6 of the tile's 128 columns, k' row t & 63.
+    // decoders of the 8-bit operand
     const int t = threadIdx.x - kSkThreads;
-    const int hh = t >> 6, kr = t & 63;
-    const int col = m0 + hh * 64;
-    const int64_t bpr = a8.cols / 64;
-    uint4 p[kSkW][4];
-    float sc[kSkW];
-    auto fetch = [&](int i) {
-#pragma unroll
-      for (int w = 0; w < kSkW; ++w) {
-        const int64_t row = static_cast<int64_t>(((kb0 + i) * kSkW + w) * 64) + kr;
-        sc[w] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) p[w][c] = make_uint4(0, 0, 0, 0);
-        if (i < nkb && row < a8.rows && col < a8.cols) {
-          const uint4* src = reinterpret_cast<const uint4*>(a8.codes + row * a8.cols + col);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) p[w][c] = __ldg(src + c);
-          sc[w] = __ldg(a8.scales + row * bpr + col / 64);
-        }
-      }
-    };
-    fetch(0);
-    for (int i = 0; i < nkb; ++i) {
-      const int s = i % kSkStages;
-      const uint32_t ph = (i / kSkStages) & 1;
-      if (!mbar_wait(&empty[s], ph ^ 1)) { *abort_flag = 1; break; }
-#pragma unroll
-      for (int w = 0; w < kSkW; ++w) {
-        uint8_t* rowp = sA + s * kSkA + w * 16384 + hh * 8192 + kr * 128;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t q[4] = {p[w][c].x, p[w][c].y, p[w][c].z, p[w][c].w};
-          uint32_t o[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t u = q[j];
-            o[2 * j] = pack_bf16x2(act8_value(static_cast<int8_t>(u), sc[w]),
-                                   act8_value(static_cast<int8_t>(u >> 8), sc[w]));
-            o[2 * j + 1] = pack_bf16x2(act8_value(static_cast<int8_t>(u >> 16), sc[w]),
-                                       act8_value(static_cast<int8_t>(u >> 24), sc[w]));
-          }
-          *reinterpret_cast<uint4*>(rowp + (((2 * c) ^ (kr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(rowp + (((2 * c + 1) ^ (kr & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[s]);
-      fetch(i + 1);
-    }
+    const A8Decoder d(a8, t % (kSkA8Group * 32), m0);
+    if (!d.run(kb0, kb1, 0, t / (kSkA8Group * 32), sA, full, lane,
+               [&](int u) { return mbar_wait(&empty[u % kSkStages], ((u / kSkStages) & 1) ^ 1); }))
+      *abort_flag = 1;
   } else if (warp >= 2) {
     // Epilogue, part 1: this split's fp32 sums into shared memory (the A ring
     // is free once the last MMA has completed).
@@ -338,10 +382,13 @@ __global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
 // one TMEM accumulator (128 x 64 fp32), warps 2..5 read it (released on
 // `tempty` per tile), scale and store.
 // ===========================================================================
-template <bool kAmn, bool kBmn>
-__global__ void __launch_bounds__(kSkThreads, 1)
-    rank_rows_kernel(const __grid_constant__ CUtensorMap tmA,
-                     const __grid_constant__ CUtensorMap tmB, SkinnyArgs args) {
+template <bool kAmn, bool kBmn, bool kA8 = false>
+__global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
+    rank_rows_kernel(const __grid_constant__ SkinnyMaps<false, kA8> maps, SkinnyArgs args, SkinnyA8 a8) {
+  static_assert(!kA8 || kAmn, "an 8-bit operand is read transposed");
+  const CUtensorMap* pA = nullptr;
+  const CUtensorMap* pB = &maps.b;
+  if constexpr (!kA8) pA = &maps.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -360,7 +407,7 @@ __global__ void __launch_bounds__(kSkThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSkStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], kA8 ? 1 + kSkA8Group : 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
@@ -381,8 +428,8 @@ __global__ void __launch_bounds__(kSkThreads, 1)
   pdl_launch_dependents();
 
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
+    if constexpr (!kA8) tma_prefetch_desc(pA);
+    tma_prefetch_desc(pB);
     int g = 0;   // stage uses over all tiles
     bool ok = true;
     for (int t = blockIdx.x; t < m_tiles && ok; t += gridDim.x) {
@@ -391,22 +438,24 @@ __global__ void __launch_bounds__(kSkThreads, 1)
         const int s = g % kSkStages;
         const uint32_t ph = (g / kSkStages) & 1;
         if (g >= kSkStages && !mbar_wait(&empty[s], ph ^ 1)) { ok = false; break; }
-        mbar_arrive_expect_tx(&full[s], kSkA + kSkB);
+        mbar_arrive_expect_tx(&full[s], kA8 ? kSkB : kSkA + kSkB);
 #pragma unroll
         for (int w = 0; w < kSkW; ++w) {
           const int kx = (i * kSkW + w) * 64;   // boxes past the end arrive as zero fill
           uint8_t* a = sA + s * kSkA + w * 16384;
           uint8_t* b = sB + s * kSkB + w * 8192;
-          if (kAmn) {
-            tma_load_2d(a, &tmA, &full[s], m0, kx);
-            tma_load_2d(a + 8192, &tmA, &full[s], m0 + 64, kx);
-          } else {
-            tma_load_2d(a, &tmA, &full[s], kx, m0);
+          if constexpr (!kA8) {
+            if (kAmn) {
+              tma_load_2d(a, pA, &full[s], m0, kx);
+              tma_load_2d(a + 8192, pA, &full[s], m0 + 64, kx);
+            } else {
+              tma_load_2d(a, pA, &full[s], kx, m0);
+            }
           }
           if (kBmn)
-            tma_load_2d(b, &tmB, &full[s], 0, kx);
+            tma_load_2d(b, pB, &full[s], 0, kx);
           else
-            tma_load_2d(b, &tmB, &full[s], kx, 0);
+            tma_load_2d(b, pB, &full[s], kx, 0);
         }
       }
     }
@@ -439,6 +488,17 @@ __global__ void __launch_bounds__(kSkThreads, 1)
       umma_commit(done);   // one phase per tile (also drains an aborted tile)
     }
     if (!ok) *abort_flag = 1;
+  } else if (kA8 && warp >= 6) {
+    // decoders of the 8-bit operand
+    const int th = threadIdx.x - kSkThreads;
+    int g = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < m_tiles && ok; t += gridDim.x, g += nkb) {
+      const A8Decoder d(a8, th % (kSkA8Group * 32), t * 128);
+      ok = d.run(0, nkb, g, th / (kSkA8Group * 32), sA, full, lane,
+                 [&](int u) { return u < kSkStages || mbar_wait(&empty[u % kSkStages], ((u / kSkStages) & 1) ^ 1); });
+    }
+    if (!ok) *abort_flag = 1;
   } else if (warp >= 2) {
     const int q = warp & 3;   // TMEM lanes 32q .. 32q + 31
     const int nc = args.ncols;
@@ -469,7 +529,8 @@ __global__ void __launch_bounds__(kSkThreads, 1)
               }
             }
           } else if (grow < args.Mp) {
-            // fp32: mode 1 out[Mp][ld], mode 2 out[nout][Mp] (consecutive lanes, consecutive rows)
+            // fp32: mode 1 out[Mp][ld], mode 2 out[nout][Mp] (consecutive lanes,
+            // consecutive rows); mode 3: bf16 out[nout][Mp]
             float* o = static_cast<float*>(args.out);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -478,6 +539,9 @@ __global__ void __launch_bounds__(kSkThreads, 1)
                 const float x = (0.0f + __uint_as_float(v[i])) * args.scale;
                 if (args.mode == 1)
                   o[static_cast<int64_t>(grow) * args.ld + cc] = x;
+                else if (args.mode == 3)
+                  static_cast<uint16_t*>(args.out)[static_cast<int64_t>(cc) * args.Mp + grow] =
+                      static_cast<uint16_t>(pack_bf16x2(x, 0.0f) & 0xFFFFu);
                 else
                   o[static_cast<int64_t>(cc) * args.Mp + grow] = x;
               }
@@ -601,13 +665,35 @@ cudaError_t run_skinny(const CUtensorMap& ta, const CUtensorMap& tb, int Mp, int
                                                  SkinnySecond{}, SkinnyA8{}, st);
 }
 
-template <bool A, bool B>
+template <bool A, bool B, bool kA8>
 cudaError_t set_rank_rows_attr() {
   static DeviceOnce once;
   return once.run([](int) {
-    return cudaFuncSetAttribute(rank_rows_kernel<A, B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(rank_rows_kernel<A, B, kA8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(kSkSmem));
   });
+}
+
+template <bool A, bool B, bool kA8>
+cudaError_t launch_rank_rows(const SkinnyMaps<false, kA8>& maps, SkinnyArgs a, int Kp, int ctas, SkinnyA8 a8,
+                             cudaStream_t st) {
+  cudaError_t e = set_rank_rows_attr<A, B, kA8>();
+  if (e != cudaSuccess) return e;
+  // at most one CTA per tile, in pairs (a 2 x 1 cluster, so that the SMs left
+  // to the fused GEMM's pairs stay in pairs)
+  const int m_tiles = (a.Mp + 127) / 128;
+  if (ctas > m_tiles) ctas = m_tiles;
+  ctas = (ctas + 1) & ~1;
+  a.nk = (Kp + 64 * kSkW - 1) / (64 * kSkW);
+  a.kb_per_split = a.nk;
+  a.splits = 1;
+  {
+    ProfScope prof(kProfSkinny, st);
+    e = launch_pdl_pair(rank_rows_kernel<A, B, kA8>, dim3(static_cast<unsigned>(ctas)),
+                        dim3(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1, 1), kSkSmem, st, maps, a, a8);
+  }
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
 }
 
 // Pairs of the fused GEMM: the fewest that keep its number of waves of tiles
@@ -639,18 +725,8 @@ template <bool kAmn, bool kBmn>
 cudaError_t run_rank_rows(const CUtensorMap& ta, const CUtensorMap& tb, int Mp, int Kp, int ncols,
                           float scale, int mode, void* out, int ld, int ctas, int32_t* d_status,
                           cudaStream_t st, int nout = -1, uint16_t* out2 = nullptr, int ld2 = 0) {
-  cudaError_t e = set_rank_rows_attr<kAmn, kBmn>();
-  if (e != cudaSuccess) return e;
-  // at most one CTA per tile, in pairs (a 2 x 1 cluster, so that the SMs left
-  // to the fused GEMM's pairs stay in pairs)
-  const int m_tiles = (Mp + 127) / 128;
-  if (ctas > m_tiles) ctas = m_tiles;
-  ctas = (ctas + 1) & ~1;
-  SkinnyArgs a;
+  SkinnyArgs a{};
   a.Mp = Mp;
-  a.nk = (Kp + 64 * kSkW - 1) / (64 * kSkW);
-  a.kb_per_split = a.nk;
-  a.splits = 1;
   a.ncols = ncols;
   a.nout = nout < 0 ? ncols : nout;
   a.scale = scale;
@@ -660,13 +736,7 @@ cudaError_t run_rank_rows(const CUtensorMap& ta, const CUtensorMap& tb, int Mp, 
   a.out2 = out2;
   a.ld2 = ld2;
   a.d_status = d_status;
-  {
-    ProfScope prof(kProfSkinny, st);
-    e = launch_pdl_pair(rank_rows_kernel<kAmn, kBmn>, dim3(static_cast<unsigned>(ctas)),
-                        dim3(kSkThreads, 1, 1), kSkSmem, st, ta, tb, a);
-  }
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return launch_rank_rows<kAmn, kBmn, false>(SkinnyMaps<false, false>{ta, tb}, a, Kp, ctas, SkinnyA8{}, st);
 }
 
 constexpr CUtensorMapDataType kBF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

@@ -16,6 +16,7 @@ import torch
 
 from . import _args
 from ._lib import QLORA_ACT_GELU, QLORA_ACT_SILU, GatedSavedC, check, lib
+from ._status import _finish, new_status
 from .act8 import Act8, act8_struct, new_act8
 
 __all__ = ["GatedSaved", "gated_forward", "gated_backward"]
@@ -34,7 +35,7 @@ class GatedSaved:
 
     @staticmethod
     def empty(M: int, N: int, r: int, save: str, device="cuda") -> "GatedSaved":
-        return _new_saved(M, N, r, save, torch.empty(0, dtype=torch.bfloat16, device=device))
+        return _new_saved(M, N, r, save, torch.empty(0, dtype=torch.bfloat16, device=device))[0]
 
     def cstruct(self, M, N, r, dev) -> GatedSavedC:
         zg = _args.tensor(self.Zg, "saved.Zg", (M, r), dev)
@@ -47,13 +48,17 @@ class GatedSaved:
 
 
 def _new_saved(M, N, r, save, like):
-    """Buffers for a GatedSaved beside `like` (a bf16 tensor)."""
+    """A new GatedSaved beside `like` (a bf16 tensor), and its C struct."""
+    if save not in ("bf16", "int8"):
+        raise ValueError("save must be None, 'bf16' or 'int8'")
+    zg, zu = like.new_empty((M, r)), like.new_empty((M, r))
     if save == "int8":
-        return GatedSaved(new_act8(M, N, like), new_act8(M, N, like), like.new_empty((M, r)), like.new_empty((M, r)))
-    if save == "bf16":
-        return GatedSaved(like.new_empty((M, N)), like.new_empty((M, N)), like.new_empty((M, r)),
-                          like.new_empty((M, r)))
-    raise ValueError("save must be None, 'bf16' or 'int8'")
+        (g, cg), (u, cu) = new_act8(M, N, like), new_act8(M, N, like)
+        return GatedSaved(g, u, zg, zu), GatedSavedC(None, None, cg.codes, cu.codes, cg.scales, cu.scales,
+                                                     zg.data_ptr(), zu.data_ptr())
+    g, u = like.new_empty((M, N)), like.new_empty((M, N))
+    return GatedSaved(g, u, zg, zu), GatedSavedC(g.data_ptr(), u.data_ptr(), None, None, None, None, zg.data_ptr(),
+                                                 zu.data_ptr())
 
 
 def _act_code(act):
@@ -82,21 +87,22 @@ def gated_forward(X, wg, wu, Ag, Bg, Au, Bu, c: float, *, act: str = "silu", sav
     it is written to instead.  wg and wu are K x N ``NF4Weight``s (either
     codebook, each with or without double quantization); Ag, Au K x r and Bg,
     Bu r x N bf16."""
-    from . import _finish, new_status
     M, K, dev = _args.cuda_2d(X, "X")
     code = _act_code(act)
     N, r, cg, cu, adapters = _weights(K, dev, wg, wu, Ag, Bg, Au, Bu)
     with _args.on(dev):
         H = _args.output(H, X, "H", (M, N))
-        if saved is None and save is not None:
-            saved = _new_saved(M, N, r, save, X)
-        kept = C.byref(saved.cstruct(M, N, r, dev)) if saved is not None else None
+        kept = None
+        if saved is not None:
+            kept = saved.cstruct(M, N, r, dev)
+        elif save is not None:
+            saved, kept = _new_saved(M, N, r, save, X)
         ws = _args.workspace(workspace, lib.qlora_gated_fwd_workspace_size(M, K, N, r), X)
         own = status is None
         status = new_status(dev) if own else status
         check(lib.qlora_gated_fwd(M, K, N, r, X.data_ptr(), C.byref(cg), C.byref(cu), *adapters, c, code,
-                                  H.data_ptr(), kept, ws.data_ptr(), ws.numel(), status.data_ptr(),
-                                  _args.stream(dev)), "qlora_gated_fwd")
+                                  H.data_ptr(), C.byref(kept) if kept is not None else None, ws.data_ptr(), ws.numel(),
+                                  status.data_ptr(), _args.stream(dev)), "qlora_gated_fwd")
         if own:
             _finish(status, own, "qlora_gated_fwd")
     return H, saved
@@ -107,7 +113,6 @@ def gated_backward(dH, X, saved: GatedSaved, wg, wu, Ag, Bg, Au, Bu, c: float, *
                    workspace=None):
     """Returns (dX, dAg, dBg, dAu, dBu); X is the forward's input or its ``Act8``.
     The adapters' gradients are of ``grad_dtype`` (fp32 or bf16)."""
-    from . import _finish, new_status
     M, N, dev = _args.cuda_2d(dH, "dH")
     code, gcode = _act_code(act), _args.grad_code(grad_dtype)
     is8 = isinstance(X, Act8)

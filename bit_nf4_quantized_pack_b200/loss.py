@@ -12,6 +12,7 @@ import torch
 
 from . import _args
 from ._lib import check, lib
+from ._status import _finish, new_status
 
 __all__ = ["head_loss_forward", "head_loss_backward"]
 
@@ -34,7 +35,6 @@ def head_loss_forward(X, w, labels, *, vocab: int | None = None, ignore_index: i
     w is the K x N ``NF4Weight`` of the head; its columns from ``vocab`` on (all
     N by default) are padding.  Rows whose label is ``ignore_index`` have loss
     0; any other label outside 0 .. vocab - 1 is a device error."""
-    from . import _finish, new_status
     M, K, N, vocab, dev, st, y = _head(X, w, labels, vocab)
     with _args.on(dev):
         loss = _args.output(loss, X, "loss", (M,), torch.float32)
@@ -54,7 +54,6 @@ def head_loss_backward(dloss, X, lse, w, labels, *, vocab: int | None = None, ig
                        dX=None, status=None, workspace=None):
     """dX (bf16 M x K) from dloss (fp32 M, the gradient of each row's loss: 1/count
     for the mean over count labels) and the forward's lse."""
-    from . import _finish, new_status
     M, K, N, vocab, dev, st, y = _head(X, w, labels, vocab)
     dl = _args.tensor(dloss, "dloss", (M,), dev, torch.float32)
     ls = _args.tensor(lse, "lse", (M,), dev, torch.float32)

@@ -429,7 +429,7 @@ qlora_status qlora_gated_bwd(int64_t M, int64_t K, int64_t N, int32_t r, const u
  *   loss, lse, dloss : fp32 M     dX : bf16 M×K
  * The logits are fp32 sums of bf16 products; the sums of exponentials, loss
  * and lse are fp32.  The backward forms the logits of a piece again, rounds
- * dloss·(softmax - onehot) to bf16 and adds the pieces' products in fp32.
+ * softmax - onehot to bf16 and adds the pieces' products, times dloss, in fp32.
  */
 size_t qlora_head_loss_fwd_workspace_size(int64_t M, int64_t K, int64_t N);
 qlora_status qlora_head_loss_fwd(int64_t M, int64_t K, int64_t N, int64_t vocab, const uint16_t* X,

@@ -80,15 +80,15 @@ def test_loss_and_gradient(M, K, vocab, kind):
 
 def test_many_pieces():
     """Enough rows that the gradient runs over several pieces of the vocabulary
-    (a piece holds about 2^25 elements), the last one ragged."""
+    (a piece holds about 2^26 elements), the last one ragged."""
     q = _q()
-    M, K, vocab = 9000, 64, 8190
+    M, K, vocab = 18000, 64, 8190
     case = Case(M, K, vocab, "dq", sigma=0.2)
     X, w, labels = case.t
     loss, lse = q.head_loss_forward(X, w, labels, vocab=vocab)
     dl = torch.from_numpy(case.dloss).cuda()
     got = q.head_loss_backward(dl, X, lse, w, labels, vocab=vocab)
-    rows = np.r_[0:40, 4480:4520, 8960:9000]
+    rows = np.r_[0:40, 8960:9000, 17960:18000]
     sub = Case.__new__(Case)
     sub.__dict__.update(case.__dict__, M=len(rows), X=case.X[rows], labels=case.labels[rows], dloss=case.dloss[rows])
     (ref_lse, dlse), dloss, (dX, err) = sub.bounds()
