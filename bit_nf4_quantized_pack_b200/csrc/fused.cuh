@@ -139,9 +139,10 @@ struct FusedArgs {
   int32_t* d_status;
 };
 
-// Split contraction of the dX modes: K-steps per item (steps * splits >= nk),
+// Tile shape of the operators' modes, and the split contraction of the dX modes: K-steps per item (steps * splits >= nk),
 // and with splits > 1 the items' sums [splits][M][Nout].
 struct SplitArgs : FusedArgs {
+  int rows;       // activation rows of a tile: 512 or 256
   int splits, steps;
   float* part;
 };
@@ -257,70 +258,100 @@ __device__ __forceinline__ void build_lut_nf4(float a, uint32_t (&H)[4], uint32_
 // What one decoder thread needs for one K-step, loaded ahead of use.
 struct RowFetch {
   uint4 p0, p1;   // 32 packed bytes of the row's NF4 block
-  float absv;     // absmax (no double quant)
+  float sv;       // absmax, or the second-level scale (double quant)
   uint32_t q;     // scale code (double quant)
-  float s2v;      // second-level scale (double quant)
   bool valid;     // row inside the weight; false also for LoRA steps
   bool second;    // the gated backward's second weight
 };
 
-// Row R of the decoded tile of CTA `rank` at K-step kk.
+// Where a decoder thread loads next: K-step kk of work item `item`, and the NF4
+// block that is its row of the decoded tile there.  Moves by additions; only at
+// the end of an item (or of the gated backward's first weight, or of the
+// contraction) does it look its block up again.
+struct RowCursor {
+  int item, kk;
+  int until;      // K-steps of the item below which `blk` moves by `stride`
+  bool valid;     // the row is inside the weight
+  bool second;    // the gated backward's second weight
+  int64_t blk, stride;
+};
+
+// Row R of the decoded tile of CTA `rank`.
 template <int kMode>
-__device__ __forceinline__ RowFetch fetch_row(const typename ModeTypes<kMode>::Args& a, int tile, int kk,
-                                              int R, int rank, int num_tiles) {
-  RowFetch f;
-  f.p0 = make_uint4(0, 0, 0, 0);
-  f.p1 = f.p0;
-  f.absv = 1.0f;
-  f.q = 0;
-  f.s2v = 1.0f;
-  f.valid = false;
-  f.second = false;
-  if (tile >= num_tiles) return f;
+__device__ __forceinline__ void seek_row(const typename ModeTypes<kMode>::Args& a, RowCursor& c, int R, int rank,
+                                         int num_items, int nsteps) {
+  c.valid = c.second = false;
+  c.until = nsteps;
+  c.blk = c.stride = 0;
+  if (c.item >= num_items) return;
+  int tile = c.item, kk = c.kk;
   if constexpr (mode_splits(kMode)) {
     const int tiles = a.m_tiles * a.n_tiles, split = tile / tiles;
     tile -= split * tiles;
     kk += split * a.steps;
+    if (kk >= a.nk) return;
+    if (a.nk - split * a.steps < nsteps) c.until = a.nk - split * a.steps;
+    if (kMode == kModeGatedBwd) {
+      const int half = a.nk / 2;
+      if (kk >= half) {
+        c.second = true;
+        kk -= half;
+      } else if (half - split * a.steps < c.until) {
+        c.until = half - split * a.steps;
+      }
+    }
   }
-  if (kk >= a.nk) return f;
   const int n0 = (tile / a.m_tiles) * mode_tile_cols(kMode);
-  const int64_t rowbytes = a.Nw / 2;
   const int64_t bpr = a.Nw / 64;
+  if constexpr (!mode_transposed(kMode)) {
+    // columns of the tile: 128 per CTA, or the same 128 of each weight
+    const int Rg = kMode == kModeGatedFwd ? R : kFBN * rank + R;
+    int col = n0 + (Rg >> 6) * 64;
+    if (col >= a.Nout) return;
+    if constexpr (mode_loss(kMode)) col += a.col0;
+    c.blk = (static_cast<int64_t>(kk) * 64 + (Rg & 63)) * bpr + col / 64;
+    c.stride = 64 * bpr;
+  } else {
+    const int kw = n0 + kFBN * rank + R;
+    if (kw >= a.Nout) return;
+    if constexpr (mode_loss(kMode)) kk += a.col0 / 64;
+    c.blk = kw * bpr + kk;
+    c.stride = 1;
+  }
+  c.valid = true;
+}
+
+// `n` steps on; consecutive items of one pair are `stride` apart.
+template <int kMode>
+__device__ __forceinline__ void advance_row(const typename ModeTypes<kMode>::Args& a, RowCursor& c, int n, int R,
+                                            int rank, int num_items, int nsteps, int stride) {
+  c.kk += n;
+  c.blk += n * c.stride;
+  if (c.kk >= c.until) {
+    while (c.kk >= nsteps) {
+      c.kk -= nsteps;
+      c.item += stride;
+    }
+    seek_row<kMode>(a, c, R, rank, num_items, nsteps);
+  }
+}
+
+// The block at the cursor.
+template <int kMode>
+__device__ __forceinline__ void fetch_row(const typename ModeTypes<kMode>::Args& a, const RowCursor& c, int rank,
+                                          RowFetch& f) {
+  f.valid = c.valid;
+  f.second = c.second;
+  if (!c.valid) return;
   const uint8_t* packed = a.packed;
   const ScaleView* sv = &a.sv;
-  if constexpr (kMode == kModeGatedFwd) {
-    if (rank != 0) { packed = a.packed2; sv = &a.sv2; }
-  }
-  if constexpr (kMode == kModeGatedBwd) {
-    if (kk >= a.nk / 2) {
-      f.second = true;
-      kk -= a.nk / 2;
+  if constexpr (mode_gated(kMode)) {
+    if (kMode == kModeGatedFwd ? rank != 0 : c.second) {
       packed = a.packed2;
       sv = &a.sv2;
     }
   }
-  int64_t blk;
-  const uint8_t* src;
-  if constexpr (!mode_transposed(kMode)) {
-    // columns of the tile: 128 per CTA, or the same 128 of each weight
-    const int Rg = kMode == kModeGatedFwd ? R : kFBN * rank + R;
-    const int nb = Rg >> 6, kr = Rg & 63;
-    if (n0 + nb * 64 >= a.Nout) return f;
-    int col = n0 + nb * 64;
-    if constexpr (mode_loss(kMode)) col += a.col0;
-    const int64_t k = static_cast<int64_t>(kk) * 64 + kr;
-    src = packed + k * rowbytes + col / 2;
-    blk = k * bpr + col / 64;
-  } else {
-    const int Rg = kFBN * rank + R;
-    if (n0 + Rg >= a.Nout) return f;
-    const int64_t kw = n0 + Rg;
-    int cb = kk;
-    if constexpr (mode_loss(kMode)) cb += a.col0 / 64;
-    src = packed + kw * rowbytes + static_cast<int64_t>(cb) * 32;
-    blk = kw * bpr + cb;
-  }
-  f.valid = true;
+  const uint8_t* src = packed + c.blk * 32;
   // volatile asm: the loads issue here, K-steps before their use, instead of
   // being moved down to it
   asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -328,31 +359,29 @@ __device__ __forceinline__ RowFetch fetch_row(const typename ModeTypes<kMode>::A
   asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(f.p1.x), "=r"(f.p1.y), "=r"(f.p1.z), "=r"(f.p1.w) : "l"(src + 16));
   if (sv->code8 == nullptr) {
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(f.absv) : "l"(sv->absmax + blk));
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(f.sv) : "l"(sv->absmax + c.blk));
   } else {
     // into a 32-bit register: a widening of a 16-bit one would wait for the load here
-    asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(f.q) : "l"(sv->code8 + blk));
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(f.s2v) : "l"(sv->s2 + (blk >> 8)));
+    asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(f.q) : "l"(sv->code8 + c.blk));
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(f.sv) : "l"(sv->s2 + (c.blk >> 8)));
   }
-  return f;
 }
 
-// Advance an iteration cursor (tile, kk) by `n` steps of nsteps per tile;
-// consecutive tiles of one pair are `stride` apart.
-__device__ __forceinline__ void advance(int& tile, int& kk, int n, int nsteps, int stride) {
-  kk += n;
-  while (kk >= nsteps) {
-    kk -= nsteps;
-    tile += stride;
-  }
+// Rows of a pair tile (the layer's own modes: always 512).
+template <int kMode>
+__device__ __forceinline__ int tile_rows(const typename ModeTypes<kMode>::Args& a) {
+  if constexpr (kMode == kModeFwd || kMode == kModeBwd)
+    return kFPairRows;
+  else
+    return a.rows;
 }
 
 // Slices of 128 rows per CTA of the tile that starts at row m0 which hold rows
 // of the activation (the layer's own modes always run both).
 template <int kMode>
-__device__ __forceinline__ int tile_slices(int M, int m0) {
+__device__ __forceinline__ int tile_slices(const typename ModeTypes<kMode>::Args& a, int m0) {
   if (kMode == kModeFwd || kMode == kModeBwd) return kFSlices;
-  return M - m0 > 256 ? 2 : 1;
+  return tile_rows<kMode>(a) > 256 && a.M - m0 > 256 ? 2 : 1;
 }
 
 // 32 fp32 values as 32 bf16 (64 bytes, 16-byte aligned)
@@ -731,9 +760,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
       for (int item = pair; item < num_tiles && ok; item += npairs) {
         int tile = item;
         const int split = split_of(tile);
-        const int m0 = (tile % args.m_tiles) * kFPairRows;
+        const int m0 = (tile % args.m_tiles) * tile_rows<kMode>(args);
         const int n0 = (tile / args.m_tiles) * kTileCols;
-        const int nh = tile_slices<kMode>(args.M, m0);
+        const int nh = tile_slices<kMode>(args, m0);
         const uint32_t act_bytes = kLayer ? kFA : static_cast<uint32_t>(nh) * 16384u;
         // (steps past the contraction's end multiply zeros by zeros: boxes past
         // the end arrive as zero fill, and so do the decoders' rows)
@@ -836,7 +865,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         int tile = item;
         const int split = split_of(tile);
         const uint32_t tph = (tc & 1) ^ 1;       // parity of the previous tile's release
-        const int nh = tile_slices<kMode>(args.M, (tile % args.m_tiles) * kFPairRows);
+        const int nh = tile_slices<kMode>(args, (tile % args.m_tiles) * tile_rows<kMode>(args));
         for (int kk = 0; kk < nsteps; ++kk) {
           if (!wait(&full_a[sa], pha) || !wait(&full_b[sb], phb)) { ok = false; break; }
           tc_fence_after();
@@ -911,14 +940,17 @@ __global__ void __launch_bounds__(kFThreads, 1)
       if (args.sv2.code8 != nullptr) off2 = __ldg(args.sv2.offset);
     }
     bool ok = true;
-    int tile = pair, kk = 0;                   // the step being decoded
-    advance(tile, kk, grp, nsteps, npairs);
-    int ptile = tile, pkk = kk;                // the step being prefetched
+    // steps still to come for this pair, and this group's among them
+    int left = pair < num_tiles ? (num_tiles - pair + npairs - 1) / npairs * nsteps - grp : 0;
+    RowCursor at{};                            // the step being loaded
+    at.item = pair + grp / nsteps * npairs;
+    at.kk = grp % nsteps;
+    seek_row<kMode>(args, at, R, rank, num_tiles, nsteps);
     uint32_t ib = static_cast<uint32_t>(grp);
     // One K-step: wait for a free weight stage, decode this thread's row.
     auto step = [&](const RowFetch& f) {
       const uint32_t s = ib % kFBStages, ph = (ib / kFBStages) & 1;
-      if (*abort_flag || !mbar_wait(&empty_b[s], ph ^ 1)) {
+      if (!mbar_try_wait(&empty_b[s], ph ^ 1) && (*abort_flag || !mbar_wait(&empty_b[s], ph ^ 1))) {
         ok = false;
         return;
       }
@@ -931,8 +963,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
           if (f.second) { sv = &args.sv2; off = off2; }
         }
         const float a = sv->code8 == nullptr
-                            ? f.absv
-                            : __fadd_rn(__fmul_rn(t8[f.q], f.s2v), off);
+                            ? f.sv
+                            : __fadd_rn(__fmul_rn(t8[f.q], f.sv), off);
         uint32_t H[4], L[4];
         build_lut(kNF4g + 16 * sv->codebook, a, H, L);
         const uint32_t pw[8] = {f.p0.x, f.p0.y, f.p0.z, f.p0.w, f.p1.x, f.p1.y, f.p1.z, f.p1.w};
@@ -947,29 +979,28 @@ __global__ void __launch_bounds__(kFThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full_b[s]), 0));
-      advance(tile, kk, kFDecGroups, nsteps, npairs);
+      left -= kFDecGroups;
       ib += kFDecGroups;
     };
     // Three prefetch slots consumed and refilled in place (no register moves
     // that would wait on loads still in flight).
-    RowFetch q0 = fetch_row<kMode>(args, ptile, pkk, R, rank, num_tiles);
-    advance(ptile, pkk, kFDecGroups, nsteps, npairs);
-    RowFetch q1 = fetch_row<kMode>(args, ptile, pkk, R, rank, num_tiles);
-    advance(ptile, pkk, kFDecGroups, nsteps, npairs);
-    RowFetch q2 = fetch_row<kMode>(args, ptile, pkk, R, rank, num_tiles);
-    advance(ptile, pkk, kFDecGroups, nsteps, npairs);
-    while (ok && tile < num_tiles) {
+    RowFetch q0{}, q1{}, q2{};
+    auto fetch = [&](RowFetch& f) {
+      fetch_row<kMode>(args, at, rank, f);
+      advance_row<kMode>(args, at, kFDecGroups, R, rank, num_tiles, nsteps, npairs);
+    };
+    fetch(q0);
+    fetch(q1);
+    fetch(q2);
+    while (ok && left > 0) {
       step(q0);
-      q0 = fetch_row<kMode>(args, ptile, pkk, R, rank, num_tiles);
-      advance(ptile, pkk, kFDecGroups, nsteps, npairs);
-      if (!ok || tile >= num_tiles) break;
+      fetch(q0);
+      if (!ok || left <= 0) break;
       step(q1);
-      q1 = fetch_row<kMode>(args, ptile, pkk, R, rank, num_tiles);
-      advance(ptile, pkk, kFDecGroups, nsteps, npairs);
-      if (!ok || tile >= num_tiles) break;
+      fetch(q1);
+      if (!ok || left <= 0) break;
       step(q2);
-      q2 = fetch_row<kMode>(args, ptile, pkk, R, rank, num_tiles);
-      advance(ptile, pkk, kFDecGroups, nsteps, npairs);
+      fetch(q2);
     }
     if (!ok) *abort_flag = 1;
   } else {
@@ -981,9 +1012,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
     for (int item = pair; item < num_tiles && ok; item += npairs, ++tc) {
       int tile = item;
       const int split = split_of(tile);
-      const int m0 = (tile % args.m_tiles) * kFPairRows;
+      const int m0 = (tile % args.m_tiles) * tile_rows<kMode>(args);
       const int n0 = (tile / args.m_tiles) * kTileCols;
-      const int nh = tile_slices<kMode>(args.M, m0);
+      const int nh = tile_slices<kMode>(args, m0);
       // loss: dloss of the lane's row in the next 32 (0 where its label does not
       // count), loaded 32 rows ahead
       auto row_scale = [&](int row) -> float {
@@ -1075,7 +1106,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
 // count busy, of at least kSplitSteps K-steps each (an item's start and its
 // sums cost about as much as four steps).
 constexpr int kSplitSteps = 8;
-constexpr int kSizingPairs = 74;
+constexpr int kSizingPairs = 74;   // whatever the device, so that results depend on the shape only
 inline int dx_most_splits(int tiles, int nk) {
   const int s = kSizingPairs / tiles, m = nk / kSplitSteps;
   const int most = s < m ? s : m;
@@ -1096,8 +1127,17 @@ inline size_t split_bytes(int64_t M, int64_t cols, int64_t nk) {
   return s > 1 ? (static_cast<size_t>(s) * M * cols * 4 + 255) / 256 * 256 : 0;
 }
 
+// Rows of the tiles of a forward layout (n_tiles column tiles): 256 where all of
+// those run at once.  A tile of 256 rows takes about 0.9 of the time of one of
+// 512 (its weights' decode is the same), so more waves of them cost more.
+inline void set_rows(SplitArgs& a) {
+  a.rows = (a.M + 255) / 256 * a.n_tiles <= kSizingPairs ? 256 : 512;
+  a.m_tiles = (a.M + a.rows - 1) / a.rows;
+}
+
 // Fills the split of a dX launch; `part` from split_bytes (null: not split).
 inline void set_split(SplitArgs& a, float* part) {
+  a.rows = kFPairRows;
   const int tiles = a.m_tiles * a.n_tiles;
   a.splits = part != nullptr ? dx_splits(tiles, a.nk) : 1;
   a.steps = (a.nk + a.splits - 1) / a.splits;

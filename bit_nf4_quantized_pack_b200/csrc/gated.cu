@@ -170,8 +170,8 @@ cudaError_t launch_gated_fwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   ga.Nw = static_cast<int>(N);
   ga.nk = static_cast<int>(K / 64);
   ga.rsteps = rsteps_of(r);
-  ga.m_tiles = tiles_of(M, kFPairRows);
   ga.n_tiles = tiles_of(N, mode_tile_cols(kModeGatedFwd));
+  set_rows(ga);
   ga.sv = w.sv_g;
   ga.packed = w.packed_g;
   ga.sv2 = w.sv_u;

@@ -99,17 +99,20 @@ cudaError_t run_loss(const CUtensorMap& act, LossArgs a, int nk, int64_t cols, c
   a.nk = nk;
   a.Nout = static_cast<int>(cols);
   a.n_tiles = static_cast<int>((cols + kFPairCols - 1) / kFPairCols);
-  set_split(a, a.part);
+  if constexpr (kMode == kModeLossDX)
+    set_split(a, a.part);
+  else
+    set_rows(a);
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   {
     ProfScope prof(kProfLoss, st);
-    e = launch_pdl_pair(fused_nf4_gemm_kernel<kMode>, dim3(2 * fused_pairs(a.m_tiles * a.n_tiles * a.splits, sms)),
+    e = launch_pdl_pair(fused_nf4_gemm_kernel<kMode>, dim3(2 * fused_pairs(a.m_tiles * a.n_tiles * (kMode == kModeLossDX ? a.splits : 1), sms)),
                         dim3(kFThreads), kFSmem, st, typename ModeTypes<kMode>::Maps{act}, a);
   }
   if (e == cudaSuccess) e = cudaGetLastError();
-  if (e == cudaSuccess && a.splits > 1) e = launch_split_join(a, kProfLoss, st);
+  if (kMode == kModeLossDX && e == cudaSuccess && a.splits > 1) e = launch_split_join(a, kProfLoss, st);
   return e;
 }
 
