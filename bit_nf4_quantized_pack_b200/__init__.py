@@ -367,8 +367,8 @@ def _linear_backward_act8(dY, X, Zc, w, A, B, c, dX, dA, dB, status, workspace, 
         own = status is None
         status = new_status(dev) if own else status
         check(lib.qlora_linear_bwd_act8(M, K, N, r, dY.data_ptr(), x16, C.byref(x8) if is8 else None, zc,
-                                        C.byref(st), pa, pb, c, dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), gcode,
-                                        ws.data_ptr(), ws.numel(), status.data_ptr(), _args.stream(dev)),
+                                        C.byref(st), pa, pb, float(c), dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), gcode,
+                                        ws.data_ptr(), ws.numel(), _args.status(status, dev), _args.stream(dev)),
               "qlora_linear_bwd_act8")
         if own:
             _finish(status, own, "qlora_linear_bwd_act8")

@@ -92,6 +92,14 @@ def grad_code(dtype):
     return GRAD_DTYPES[dtype]
 
 
+def status(given, dev):
+    """The address of the caller's status word."""
+    if (not isinstance(given, torch.Tensor) or given.dtype is not torch.int32 or given.device != dev
+            or given.numel() < 1):
+        raise TypeError(f"status must be an int32 tensor on {dev} (see new_status)")
+    return given.data_ptr()
+
+
 def workspace(given, nbytes, like):
     """The caller's workspace, or a new one from the caching allocator: it is
     ordered on the current stream, and under graph capture it belongs to that

@@ -70,7 +70,7 @@ def act8_quantize(X: torch.Tensor, *, out: Act8 | None = None, status: torch.Ten
             st = act8_struct(out, "out", M, K, dev)
         own = status is None
         status = new_status(dev) if own else status
-        check(lib.qlora_act8_quantize(X.data_ptr(), C.byref(st), status.data_ptr(), _args.stream(dev)),
+        check(lib.qlora_act8_quantize(X.data_ptr(), C.byref(st), _args.status(status, dev), _args.stream(dev)),
               "qlora_act8_quantize")
         if own:
             _finish(status, own, "qlora_act8_quantize")

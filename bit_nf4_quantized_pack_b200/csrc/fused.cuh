@@ -941,7 +941,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     }
     bool ok = true;
     // steps still to come for this pair, and this group's among them
-    int left = pair < num_tiles ? (num_tiles - pair + npairs - 1) / npairs * nsteps - grp : 0;
+    int64_t left = pair < num_tiles ? static_cast<int64_t>((num_tiles - pair + npairs - 1) / npairs) * nsteps - grp : 0;
     RowCursor at{};                            // the step being loaded
     at.item = pair + grp / nsteps * npairs;
     at.kk = grp % nsteps;

@@ -125,6 +125,8 @@ cudaError_t launch_gated_fwd(int64_t M, int64_t K, int64_t N, int r, const uint1
                              const GatedWeights& w, uint16_t* H, const GatedKept& kept, void* ws,
                              size_t ws_bytes, int32_t* d_status, cudaStream_t st, int num_sms) {
   (void)num_sms;
+  // up to 128 rows: 73 us there against 79 for 129 here at 4096 x 11008 (and 35
+  // against 79 for one row)
   if (gated_rows_fit(M, K, N)) return launch_gated_rows(M, K, N, r, X, w, H, kept, ws, ws_bytes, d_status, st);
   WsCursor cur{static_cast<char*>(ws), ws_bytes};
   const int rp = padded_rank(r);
@@ -297,9 +299,13 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
 
   // dX first, then dA and dB (which need only dZ, Z, X, dG and dU) on the
   // library's stream, so that they take the SMs dX leaves idle; the caller's
-  // stream waits for them before the call returns.
+  // stream waits for them before the call returns.  Small steps run in order:
+  // the fork and the join cost more than they hide (the whole step at 333 x 1088
+  // x 2752 100 us forked, 89 in order; at 700 x 4096 x 4096 158 and 159; at 1500 x
+  // 4096 x 11008 500 and 533).
   std::lock_guard<std::mutex> lock(g_side_mu);
-  SideStream* ss = prof_timing(kProfSkinny) ? nullptr : side_stream(dev);
+  SideStream* ss =
+      prof_timing(kProfSkinny) || !worth_forking(M, K, N) ? nullptr : side_stream(dev);
   cudaStream_t s2 = st;
   if (ss != nullptr && cudaEventRecord(ss->fork, st) == cudaSuccess) s2 = ss->s;
   {

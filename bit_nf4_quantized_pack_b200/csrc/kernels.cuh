@@ -167,6 +167,11 @@ struct SideStream {
   cudaEvent_t fork = nullptr, join = nullptr;
 };
 extern std::mutex g_side_mu;
+// Whether a backward's dX (M x K over N) is long enough to run its adapter
+// gradients beside it on that stream.
+inline bool worth_forking(int64_t M, int64_t K, int64_t N) {
+  return static_cast<double>(M) * K * N >= 1e10;
+}
 SideStream* side_stream(int dev);
 
 // linear.cu — forward and backward of the layer

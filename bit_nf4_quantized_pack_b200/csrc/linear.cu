@@ -278,7 +278,9 @@ cudaError_t launch_linear_bwd(int64_t M, int64_t K, int64_t N, int r, const uint
   // partial last wave of tiles leaves idle.  The caller's stream then waits
   // for them: to the caller the call is ordered as one operation on st.
   std::lock_guard<std::mutex> lock(g_side_mu);
-  SideStream* ss = prof_timing(kProfSkinny) ? nullptr : side_stream(dev);
+  // (in order for the smaller backwards of an 8-bit input or with bf16 gradients)
+  const bool in_order = (X8 != nullptr || grad_bf16) && !worth_forking(M, K, N);
+  SideStream* ss = prof_timing(kProfSkinny) || in_order ? nullptr : side_stream(dev);
   cudaStream_t s2 = st;
   if (ss != nullptr && cudaEventRecord(ss->fork, st) == cudaSuccess) s2 = ss->s;
   {

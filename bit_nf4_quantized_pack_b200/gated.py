@@ -100,9 +100,9 @@ def gated_forward(X, wg, wu, Ag, Bg, Au, Bu, c: float, *, act: str = "silu", sav
         ws = _args.workspace(workspace, lib.qlora_gated_fwd_workspace_size(M, K, N, r), X)
         own = status is None
         status = new_status(dev) if own else status
-        check(lib.qlora_gated_fwd(M, K, N, r, X.data_ptr(), C.byref(cg), C.byref(cu), *adapters, c, code,
+        check(lib.qlora_gated_fwd(M, K, N, r, X.data_ptr(), C.byref(cg), C.byref(cu), *adapters, float(c), code,
                                   H.data_ptr(), C.byref(kept) if kept is not None else None, ws.data_ptr(), ws.numel(),
-                                  status.data_ptr(), _args.stream(dev)), "qlora_gated_fwd")
+                                  _args.status(status, dev), _args.stream(dev)), "qlora_gated_fwd")
         if own:
             _finish(status, own, "qlora_gated_fwd")
     return H, saved
@@ -135,9 +135,9 @@ def gated_backward(dH, X, saved: GatedSaved, wg, wu, Ag, Bg, Au, Bu, c: float, *
         own = status is None
         status = new_status(dev) if own else status
         check(lib.qlora_gated_bwd(M, K, N, r, dH.data_ptr(), x16, C.byref(x8) if is8 else None, C.byref(kept),
-                                  C.byref(cg), C.byref(cu), *adapters, c, code, dX.data_ptr(), dAg.data_ptr(),
+                                  C.byref(cg), C.byref(cu), *adapters, float(c), code, dX.data_ptr(), dAg.data_ptr(),
                                   dBg.data_ptr(), dAu.data_ptr(), dBu.data_ptr(), gcode, ws.data_ptr(), ws.numel(),
-                                  status.data_ptr(), _args.stream(dev)), "qlora_gated_bwd")
+                                  _args.status(status, dev), _args.stream(dev)), "qlora_gated_bwd")
         if own:
             _finish(status, own, "qlora_gated_bwd")
     return dX, dAg, dBg, dAu, dBu

@@ -44,7 +44,7 @@ def head_loss_forward(X, w, labels, *, vocab: int | None = None, ignore_index: i
         status = new_status(dev) if own else status
         check(lib.qlora_head_loss_fwd(M, K, N, vocab, X.data_ptr(), C.byref(st), y, int(ignore_index),
                                       loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(),
-                                      status.data_ptr(), _args.stream(dev)), "qlora_head_loss_fwd")
+                                      _args.status(status, dev), _args.stream(dev)), "qlora_head_loss_fwd")
         if own:
             _finish(status, own, "qlora_head_loss_fwd")
     return loss, lse
@@ -63,7 +63,7 @@ def head_loss_backward(dloss, X, lse, w, labels, *, vocab: int | None = None, ig
         own = status is None
         status = new_status(dev) if own else status
         check(lib.qlora_head_loss_bwd(M, K, N, vocab, dl, X.data_ptr(), ls, C.byref(st), y, int(ignore_index),
-                                      dX.data_ptr(), ws.data_ptr(), ws.numel(), status.data_ptr(),
+                                      dX.data_ptr(), ws.data_ptr(), ws.numel(), _args.status(status, dev),
                                       _args.stream(dev)), "qlora_head_loss_bwd")
         if own:
             _finish(status, own, "qlora_head_loss_bwd")

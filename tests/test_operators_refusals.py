@@ -205,7 +205,9 @@ def test_wrappers_refuse_wrong_shapes_and_short_buffers(q):
                  lambda: q.gated_backward(dH, X, saved_, *args, dX=t(8, 64, dtype=torch.float32)),
                  lambda: q.gated_backward(dH, X, (H, H), *args),
                  lambda: q.head_loss_forward(X, w, torch.zeros(8, dtype=torch.int32, device="cuda")),
-                 lambda: q.act8_quantize(t(8, 128)[:, ::2])):
+                 lambda: q.act8_quantize(t(8, 128)[:, ::2]),
+                 lambda: q.act8_quantize(X, status=torch.zeros(1, dtype=torch.int32)),
+                 lambda: q.gated_forward(X, *args, status=t(1))):
         with pytest.raises(TypeError):
             call()
     for call in (lambda: q.act8_quantize(t(8, 96)), lambda: q.act8_quantize(t(0, 64)),
