@@ -66,39 +66,73 @@ __device__ __forceinline__ float act8_scale(float amax) {
   const float s = __fmaf_rn(__fmaf_rn(-127.0f, q, amax), r, q);
   return s >= FLT_MIN ? s : 1.0f;
 }
-// a factor for act8_round: 1 / s within 2^-23
+// a factor for act8_round: 1 / s within two units in the last place (2^-22)
 __device__ __forceinline__ float act8_inverse(float s) { return __fdividef(1.0f, s); }
 
-// rint(fl32(x / s)), in two steps.  x * inv is within 127 * 2^-22 of x / s (the
-// inverse's error and one rounding, of a magnitude of at most 127), so both round alike unless the
-// product is within 2^-14 of a tie: act8_round rounds it (by the addition of 1.5
-// * 2^23, whose low byte then holds the code) and notes a near tie, and only for
-// a block of values with one does act8_exact carry the divisions out.
+// rint(fl32(x / s)): the product with the inverse, t, and one step with its exact
+// remainder, t + (x - t s) / s, give fl32(x / s), and the addition of 1.5 *
+// 2^23 rounds that to an integer in the low byte.  (By enumeration of the bf16
+// magnitudes of x and of the block's largest, for every inverse within four units
+// in the last place of 1 / s.  Below kAct8Tiny the remainder can be subnormal and
+// inexact: there the divisions are carried out.)  A test for values near a tie
+// with a division for those few was slower: an x and a largest magnitude of 8 bits
+// each often meet a tie, 1.4 values in a thousand.  The arithmetic is packed, two
+// values an instruction: the codec is bound by the instructions it issues.
 constexpr float kAct8Magic = 12582912.0f;
-__device__ __forceinline__ uint32_t act8_round(float x, float inv, bool& near) {
-  const float t = x * inv;
-  const float r = __fadd_rn(t, kAct8Magic);
-  near |= fabsf(__fadd_rn(t, -__fadd_rn(r, -kAct8Magic))) > 0.5f - 6.103515625e-05f;
-  return __float_as_uint(r);
+constexpr float kAct8Tiny = 1.0f / (1ull << 50) / (1ull << 50);   // 2^-100
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 __device__ __forceinline__ uint32_t act8_exact(float x, float s) {
   return __float_as_uint(__fadd_rn(rintf(__fdiv_rn(x, s)), kAct8Magic));
 }
-// four results of these as four code bytes
+// the low bytes of four words
 __device__ __forceinline__ uint32_t act8_pack(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
-// the codes of four values
-__device__ __forceinline__ uint32_t act8_codes4(const float (&x)[4], float s, float inv) {
-  bool near = false;
-  uint32_t r[4];
+// the codes of 2 n bf16 values, each in the low byte of a word (inv = act8_inverse(s))
+template <int n>
+__device__ __forceinline__ void act8_round(const uint32_t (&w)[n], float s, float inv, uint32_t (&r)[2 * n]) {
+  const uint64_t inv2 = f32x2(inv, inv), minus_s = f32x2(-s, -s), magic2 = f32x2(kAct8Magic, kAct8Magic);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = act8_round(x[i], inv, near);
-  if (near) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = act8_exact(x[i], s);
+  for (int k = 0; k < n; ++k) {
+    const uint64_t x = f32x2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+    const uint64_t t = mul_f32x2(x, inv2);
+    const uint64_t q = add_f32x2(fma_f32x2(fma_f32x2(t, minus_s, x), inv2, t), magic2);
+    r[2 * k] = static_cast<uint32_t>(q);
+    r[2 * k + 1] = static_cast<uint32_t>(q >> 32);
   }
-  return act8_pack(r[0], r[1], r[2], r[3]);
+  if (s < kAct8Tiny) {
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      r[2 * k] = act8_exact(__uint_as_float(w[k] << 16), s);
+      r[2 * k + 1] = act8_exact(__uint_as_float(w[k] & 0xFFFF0000u), s);
+    }
+  }
+}
+// sixteen values' codes
+__device__ __forceinline__ uint4 act8_codes16(const uint32_t (&w)[8], float s, float inv) {
+  uint32_t r[16];
+  act8_round(w, s, inv, r);
+  return make_uint4(act8_pack(r[0], r[1], r[2], r[3]), act8_pack(r[4], r[5], r[6], r[7]),
+                    act8_pack(r[8], r[9], r[10], r[11]), act8_pack(r[12], r[13], r[14], r[15]));
 }
 
 // The values of four codes before their rounding to bf16, fl32(code * s).  A code

@@ -51,15 +51,9 @@ __global__ void __launch_bounds__(kThreads)
       bad |= top >= 0x7F80u;
       const float s = act8_scale(__uint_as_float(top << 16));
       const float inv = act8_inverse(s);
-      uint32_t o[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float v[4] = {__uint_as_float(w[2 * k] << 16), __uint_as_float(w[2 * k] & 0xFFFF0000u),
-                            __uint_as_float(w[2 * k + 1] << 16), __uint_as_float(w[2 * k + 1] & 0xFFFF0000u)};
-        o[k] = act8_codes4(v, s, inv);
-      }
+      const uint4 o = act8_codes16(w, s, inv);
       if (i < pieces) {
-        codes[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        codes[i] = o;
         if ((lane & 3) == 0) scales[i >> 2] = s;
       }
     }

@@ -120,6 +120,9 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 
 // 16 bytes to a shared-memory address (an aligned-up generic pointer would
 // make this a generic store with 64-bit address arithmetic)
+__device__ __forceinline__ void sts16(uint32_t saddr, uint32_t v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(saddr), "h"(static_cast<uint16_t>(v)) : "memory");
+}
 __device__ __forceinline__ void sts128(uint32_t saddr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
@@ -227,11 +230,10 @@ __device__ __forceinline__ void bulk_load_1d(void* smem_dst, const void* gsrc, u
 
 // shared -> global tiled store (bulk-group completion); the tile's generic
 // writes must be made visible to the async proxy first (fence_proxy_async_smem)
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* smem_src, int32_t x,
-                                             int32_t y) {
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t smem_src, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(smem_src)), "r"(x), "r"(y)
+               "r"(smem_src), "r"(x), "r"(y)
                : "memory");
 }
 

@@ -166,6 +166,15 @@ cudaError_t launch_gated_fwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   if (!make_tmap_2d(&maps.la2, copy ? Zwu : Zu, kBF16, 2, M, rp, rp, 64, 128, kSW128)) return cudaErrorInvalidValue;
   if (!make_tmap_2d(&maps.lb, w.Bg, kBF16, 2, r, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
   if (!make_tmap_2d(&maps.lb2, w.Bu, kBF16, 2, r, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&maps.out, H, kBF16, 2, M, N, N, 32, 32, kSW64)) return cudaErrorInvalidValue;
+  maps.g = maps.u = maps.out;
+  if (kept.G != nullptr) {
+    if (!make_tmap_2d(&maps.g, kept.G, kBF16, 2, M, N, N, 32, 32, kSW64)) return cudaErrorInvalidValue;
+    if (!make_tmap_2d(&maps.u, kept.U, kBF16, 2, M, N, N, 32, 32, kSW64)) return cudaErrorInvalidValue;
+  } else if (kept.G8 != nullptr) {
+    if (!make_tmap_2d(&maps.g, kept.G8, kU8, 1, M, N, N, 64, 32, kSW64)) return cudaErrorInvalidValue;
+    if (!make_tmap_2d(&maps.u, kept.U8, kU8, 1, M, N, N, 64, 32, kSW64)) return cudaErrorInvalidValue;
+  }
   GatedArgs ga{};
   ga.M = iM;
   ga.Nout = static_cast<int>(N);
@@ -178,12 +187,8 @@ cudaError_t launch_gated_fwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   ga.packed = w.packed_g;
   ga.sv2 = w.sv_u;
   ga.packed2 = w.packed_u;
-  ga.out = H;
   ga.act = w.act;
-  ga.G = kept.G;
-  ga.U = kept.U;
-  ga.G8 = kept.G8;
-  ga.U8 = kept.U8;
+  ga.keep = kept.G != nullptr ? 1 : (kept.G8 != nullptr ? 2 : 0);
   ga.Gs = kept.Gs;
   ga.Us = kept.Us;
   ga.d_status = d_status;
@@ -193,8 +198,8 @@ cudaError_t launch_gated_fwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   const int grid = fused_pairs(ga.m_tiles * ga.n_tiles, sms);
   {
     ProfScope prof(kProfGated, st);
-    e = launch_pdl_pair(fused_nf4_gemm_kernel<kModeGatedFwd>, dim3(2 * grid), dim3(kFThreads), kFSmem, st,
-                        maps, ga);
+    e = launch_pdl_pair(fused_nf4_gemm_kernel<kModeGatedFwd>, dim3(2 * grid), dim3(kFThreads),
+                        kFSmem, st, maps, ga);
   }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
@@ -268,6 +273,7 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   if (!make_tmap_2d(&maps.la2, dZu, kBF16, 2, M, rp, rp, 64, 128, kSW128)) return cudaErrorInvalidValue;
   if (!make_tmap_2d(&maps.lb, Ag, kBF16, 2, K, rp, rp, 64, kFBN, kSW128)) return cudaErrorInvalidValue;
   if (!make_tmap_2d(&maps.lb2, Au, kBF16, 2, K, rp, rp, 64, kFBN, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&maps.out, dX, kBF16, 2, M, K, K, 32, 32, kSW64)) return cudaErrorInvalidValue;
   GatedArgs ga{};
   ga.M = iM;
   ga.Nout = iK;
@@ -280,7 +286,6 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   ga.packed = w.packed_g;
   ga.sv2 = w.sv_u;
   ga.packed2 = w.packed_u;
-  ga.out = dX;
   ga.d_status = d_status;
   set_split(ga, part);
   int dev = 0, sms = 148;
@@ -314,7 +319,7 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
                         maps, ga);
   }
   if (e == cudaSuccess) e = cudaGetLastError();
-  if (e == cudaSuccess && ga.splits > 1) e = launch_split_join(ga, kProfGated, st);
+  if (e == cudaSuccess && ga.splits > 1) e = launch_split_join(ga, dX, kProfGated, st);
   if (s2 != st) {
     const cudaError_t ew = cudaStreamWaitEvent(s2, ss->fork, 0);
     if (ew != cudaSuccess) {

@@ -583,9 +583,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) amax = fmax_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
       const float s = act8_scale(amax), inv = act8_inverse(s);
-      const float x[4] = {x0, x1, 0.0f, 0.0f};
+      const uint32_t x[1] = {w == 0 ? pack_bf16x2(g2.x, g2.y) : pack_bf16x2(u2.x, u2.y)};
+      uint32_t q[2];
+      act8_round(x, s, inv, q);
       *reinterpret_cast<uint16_t*>((w == 0 ? a.kept.G8 : a.kept.U8) + at) =
-          static_cast<uint16_t>(act8_codes4(x, s, inv));
+          static_cast<uint16_t>(__byte_perm(q[0], q[1], 0x0040));
       if (lane == 0) {
         (w == 0 ? a.kept.Gs : a.kept.Us)[row * (a.N / 64) + n / 64] = s;
         if (!(amax <= FLT_MAX)) raise_status(a.d_status, QLORA_ERR_NONFINITE);

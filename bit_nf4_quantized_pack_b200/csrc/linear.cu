@@ -103,7 +103,7 @@ cudaError_t launch_linear_fwd(int64_t M, int64_t K, int64_t N, int r, const uint
   }
   if (!cur.ok) return cudaErrorInvalidValue;
   // Zc = bf16(c * X A): A operand X (K-major), B operand A (MN-major over r)
-  CUtensorMap tX, tAl, tZc, tBl;
+  CUtensorMap tX, tAl, tZc, tBl, tY;
   if (!make_tmap_2d(&tX, X, kBF16, 2, M, K, K, 64, 128, kSW128)) return cudaErrorInvalidValue;
   if (!make_tmap_2d(&tAl, At, kBF16, 2, K, rp, rp, 64, 64, kSW128)) return cudaErrorInvalidValue;
   if (M <= 16) {
@@ -139,6 +139,7 @@ cudaError_t launch_linear_fwd(int64_t M, int64_t K, int64_t N, int r, const uint
   if (e != cudaSuccess) return e;
   if (!make_tmap_2d(&tZc, pad ? Zp : Zc, kBF16, 2, M, rp, rp, 64, 128, kSW128)) return cudaErrorInvalidValue;
   if (!make_tmap_2d(&tBl, B, kBF16, 2, r, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&tY, Y, kBF16, 2, M, N, N, 32, 32, kSW64)) return cudaErrorInvalidValue;
   FusedArgs fa;
   fa.M = static_cast<int>(M);
   fa.Nout = static_cast<int>(N);
@@ -149,7 +150,6 @@ cudaError_t launch_linear_fwd(int64_t M, int64_t K, int64_t N, int r, const uint
   fa.n_tiles = static_cast<int>((N + kFPairCols - 1) / kFPairCols);   // and 256 columns
   fa.sv = sv;
   fa.packed = packed;
-  fa.out = Y;
   fa.d_status = d_status;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
@@ -159,8 +159,8 @@ cudaError_t launch_linear_fwd(int64_t M, int64_t K, int64_t N, int r, const uint
   const int grid = fused_pairs(fa.m_tiles * fa.n_tiles, sms);
   {
     ProfScope prof(kProfFusedFwd, st);
-    e = launch_pdl_pair(fused_nf4_gemm_kernel<kModeFwd>, dim3(2 * grid), dim3(kFThreads), kFSmem, st,
-                        ModeTypes<kModeFwd>::Maps{tX, tZc, tBl}, fa);
+    e = launch_pdl_pair(fused_nf4_gemm_kernel<kModeFwd>, dim3(2 * grid), dim3(kFThreads), kFSmem,
+                        st, ModeTypes<kModeFwd>::Maps{tX, tZc, tBl, tY}, fa);
   }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
@@ -254,6 +254,8 @@ cudaError_t launch_linear_bwd(int64_t M, int64_t K, int64_t N, int r, const uint
   if (!make_tmap_2d(&tAl, At, kBF16, 2, K, rp, rp, 64, kFBN, kSW128)) return cudaErrorInvalidValue;
   CUtensorMap tdZa;
   if (!make_tmap_2d(&tdZa, dZ, kBF16, 2, M, rp, rp, 64, 128, kSW128)) return cudaErrorInvalidValue;
+  CUtensorMap tdX;
+  if (!make_tmap_2d(&tdX, dX, kBF16, 2, M, K, K, 32, 32, kSW64)) return cudaErrorInvalidValue;
   FusedArgs fa;
   fa.M = static_cast<int>(M);
   fa.Nout = static_cast<int>(K);
@@ -264,7 +266,6 @@ cudaError_t launch_linear_bwd(int64_t M, int64_t K, int64_t N, int r, const uint
   fa.n_tiles = static_cast<int>((K + kFPairCols - 1) / kFPairCols);   // and 256 output columns
   fa.sv = sv;
   fa.packed = packed;
-  fa.out = dX;
   fa.d_status = d_status;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
@@ -286,7 +287,7 @@ cudaError_t launch_linear_bwd(int64_t M, int64_t K, int64_t N, int r, const uint
   {
     ProfScope prof(kProfFusedBwd, st);
     e = launch_pdl_pair(fused_nf4_gemm_kernel<kModeBwd>, dim3(2 * grid), dim3(kFThreads), kFSmem, st,
-                        ModeTypes<kModeBwd>::Maps{tG, tdZa, tAl}, fa);
+                        ModeTypes<kModeBwd>::Maps{tG, tdZa, tAl, tdX}, fa);
   }
   if (e == cudaSuccess) e = cudaGetLastError();
   if (s2 != st) {

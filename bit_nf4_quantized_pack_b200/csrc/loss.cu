@@ -5,7 +5,7 @@
 //   l = X·Ŵ,  lse_i = log Σ_v exp(l_iv),  loss_i = lse_i - l_i[y_i]
 //   dX_i = dloss_i (Σ_v softmax(l_i)_v Ŵ_v - Ŵ_{y_i})
 //
-// Forward: the fused GEMM's epilogue reduces each 256 columns of a row to
+// Forward: the fused GEMM's epilogue reduces each 128 columns of a row to
 // their maximum and sum of exponentials (kModeLossStats); a second kernel joins
 // those.  Backward: per piece of columns the logits are formed again and the
 // epilogue writes P = bf16(exp(l - lse) - onehot) (kModeLossGrad); a fused GEMM
@@ -33,12 +33,12 @@ int64_t piece_cols(int64_t M, int64_t N) {
   return (per + 255) / 256 * 256;
 }
 
-// Joins the (maximum, sum) pairs of a row's column tiles: 32 rows x 8 slices
-// of the tiles per block.
+// Joins the (maximum, sum) pairs of a row: 32 rows x 8 slices of the pairs per
+// block.
 constexpr int kJoinRows = 32, kJoinSlices = 8;
 __global__ void __launch_bounds__(kJoinRows * kJoinSlices)
     loss_join_kernel(const float2* __restrict__ stats, const float* __restrict__ label_logit, int M,
-                     int n_tiles, int64_t vocab, const int64_t* __restrict__ labels, int64_t ignore_index,
+                     int nstats, int64_t vocab, const int64_t* __restrict__ labels, int64_t ignore_index,
                      float* __restrict__ loss, float* __restrict__ lse, int32_t* d_status) {
   __shared__ float sm[kJoinSlices][kJoinRows], ss[kJoinSlices][kJoinRows];
   pdl_launch_dependents();
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kJoinRows * kJoinSlices)
     m = nm;
   };
   if (row < M)
-    for (int t = sl; t < n_tiles; t += kJoinSlices) {
+    for (int t = sl; t < nstats; t += kJoinSlices) {
       const float2 p = stats[static_cast<int64_t>(t) * M + row];
       add(p.x, p.y);
     }
@@ -93,7 +93,8 @@ LossArgs loss_args(int64_t M, int64_t N, int64_t vocab, const uint8_t* packed, S
 }
 
 template <int kMode>
-cudaError_t run_loss(const CUtensorMap& act, LossArgs a, int nk, int64_t cols, cudaStream_t st) {
+cudaError_t run_loss(const CUtensorMap& act, const CUtensorMap& out, LossArgs a, int nk, int64_t cols, cudaStream_t st,
+                     uint16_t* dX = nullptr) {
   cudaError_t e = set_fused_attr<kMode>();
   if (e != cudaSuccess) return e;
   a.nk = nk;
@@ -109,17 +110,17 @@ cudaError_t run_loss(const CUtensorMap& act, LossArgs a, int nk, int64_t cols, c
   {
     ProfScope prof(kProfLoss, st);
     e = launch_pdl_pair(fused_nf4_gemm_kernel<kMode>, dim3(2 * fused_pairs(a.m_tiles * a.n_tiles * (kMode == kModeLossDX ? a.splits : 1), sms)),
-                        dim3(kFThreads), kFSmem, st, typename ModeTypes<kMode>::Maps{act}, a);
+                        dim3(kFThreads), kFSmem, st, typename ModeTypes<kMode>::Maps{act, out}, a);
   }
   if (e == cudaSuccess) e = cudaGetLastError();
-  if (kMode == kModeLossDX && e == cudaSuccess && a.splits > 1) e = launch_split_join(a, kProfLoss, st);
+  if (kMode == kModeLossDX && e == cudaSuccess && a.splits > 1) e = launch_split_join(a, dX, kProfLoss, st);
   return e;
 }
 
 }  // namespace
 
 size_t loss_fwd_workspace_bytes(int64_t M, int64_t N) {
-  return align256(static_cast<size_t>((N + kFPairCols - 1) / kFPairCols) * M * sizeof(float2)) +
+  return align256(static_cast<size_t>((N + kFPairCols - 1) / kFPairCols * 2) * M * sizeof(float2)) +
          align256(static_cast<size_t>(M) * 4);
 }
 
@@ -138,7 +139,7 @@ cudaError_t launch_loss_fwd(int64_t M, int64_t K, int64_t N, int64_t vocab, cons
   WsCursor cur{static_cast<char*>(ws), ws_bytes};
   // only the tiles that hold columns of the vocabulary
   const int n_tiles = static_cast<int>((vocab + kFPairCols - 1) / kFPairCols);
-  float2* stats = static_cast<float2*>(cur.take(static_cast<size_t>(n_tiles) * M * sizeof(float2)));
+  float2* stats = static_cast<float2*>(cur.take(static_cast<size_t>(2 * n_tiles) * M * sizeof(float2)));
   float* lab = static_cast<float*>(cur.take(static_cast<size_t>(M) * 4));
   if (!cur.ok) return cudaErrorInvalidValue;
   CUtensorMap tX;
@@ -147,13 +148,13 @@ cudaError_t launch_loss_fwd(int64_t M, int64_t K, int64_t N, int64_t vocab, cons
   a.stats = stats;
   a.label_logit = lab;
   const int64_t cols = static_cast<int64_t>(n_tiles) * kFPairCols < N ? static_cast<int64_t>(n_tiles) * kFPairCols : N;
-  cudaError_t e = run_loss<kModeLossStats>(tX, a, static_cast<int>(K / 64), cols, st);
+  cudaError_t e = run_loss<kModeLossStats>(tX, tX, a, static_cast<int>(K / 64), cols, st);
   if (e != cudaSuccess) return e;
   {
     ProfScope prof(kProfLoss, st);
     e = launch_pdl(loss_join_kernel, dim3(static_cast<unsigned>((M + kJoinRows - 1) / kJoinRows)),
                    dim3(kJoinRows * kJoinSlices), 0, st, 1, static_cast<const float2*>(stats),
-                   static_cast<const float*>(lab), static_cast<int>(M), n_tiles, vocab, labels,
+                   static_cast<const float*>(lab), static_cast<int>(M), 2 * n_tiles, vocab, labels,
                    ignore_index, loss, lse, d_status);
   }
   if (e != cudaSuccess) return e;
@@ -175,6 +176,8 @@ cudaError_t launch_loss_bwd(int64_t M, int64_t K, int64_t N, int64_t vocab, cons
   if (!cur.ok) return cudaErrorInvalidValue;
   CUtensorMap tX;
   if (!make_tmap_2d(&tX, X, kBF16, 2, M, K, K, 64, 128, kSW128)) return cudaErrorInvalidValue;
+  CUtensorMap tdX;
+  if (!make_tmap_2d(&tdX, dX, kBF16, 2, M, K, K, 32, 32, kSW64)) return cudaErrorInvalidValue;
   // whole 64-blocks of the vocabulary; the head's columns behind them add nothing
   const int64_t end = (vocab + 63) / 64 * 64;
   for (int64_t c0 = 0; c0 < end; c0 += per) {
@@ -183,17 +186,17 @@ cudaError_t launch_loss_bwd(int64_t M, int64_t K, int64_t N, int64_t vocab, cons
     a.col0 = static_cast<int>(c0);
     a.lse = lse;
     a.dloss = dloss;
-    a.out = P;
-    cudaError_t e = run_loss<kModeLossGrad>(tX, a, static_cast<int>(K / 64), cols, st);
+    CUtensorMap tPout;
+    if (!make_tmap_2d(&tPout, P, kBF16, 2, M, cols, cols, 32, 32, kSW64)) return cudaErrorInvalidValue;
+    cudaError_t e = run_loss<kModeLossGrad>(tX, tPout, a, static_cast<int>(K / 64), cols, st);
     if (e != cudaSuccess) return e;
     CUtensorMap tP;
     if (!make_tmap_2d(&tP, P, kBF16, 2, M, cols, cols, 64, 128, kSW128)) return cudaErrorInvalidValue;
-    a.out = dX;
     a.part = part;
     a.acc = acc;
     a.first = c0 == 0 ? 1 : 0;
     a.last = c0 + cols >= end ? 1 : 0;
-    e = run_loss<kModeLossDX>(tP, a, static_cast<int>(cols / 64), K, st);
+    e = run_loss<kModeLossDX>(tP, tdX, a, static_cast<int>(cols / 64), K, st, dX);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

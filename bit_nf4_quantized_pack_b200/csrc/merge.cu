@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && n0 + 64 * bb < a.N && k0 + 32 * q < a.K) {   // boxes wholly outside: no store
-          tma_store_2d(&tmO, so, n0 + 64 * bb, k0 + 32 * q);
+          tma_store_2d(&tmO, smem_u32(so), n0 + 64 * bb, k0 + 32 * q);
           bulk_commit_group();
         }
       }

@@ -740,7 +740,9 @@ cudaError_t run_rank_rows(const CUtensorMap& ta, const CUtensorMap& tb, int Mp, 
 }
 
 constexpr CUtensorMapDataType kBF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
 constexpr CUtensorMapSwizzle kSW128 = CU_TENSOR_MAP_SWIZZLE_128B;
+constexpr CUtensorMapSwizzle kSW64 = CU_TENSOR_MAP_SWIZZLE_64B;
 
 int rsteps_of(int r) { return (r + 15) / 16; }
 
