@@ -140,10 +140,15 @@ __device__ __forceinline__ uint4 act8_codes16(const uint32_t (&w)[8], float s, f
 // exact), since the conversion instruction runs at a quarter of the rate.
 __device__ __forceinline__ void act8_values4(uint32_t codes, float s, float (&v)[4]) {
   const uint32_t u = codes ^ 0x80808080u;
-  v[0] = __fmul_rn(__fadd_rn(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540)), -8388736.0f), s);
-  v[1] = __fmul_rn(__fadd_rn(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7541)), -8388736.0f), s);
-  v[2] = __fmul_rn(__fadd_rn(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7542)), -8388736.0f), s);
-  v[3] = __fmul_rn(__fadd_rn(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7543)), -8388736.0f), s);
+  const uint64_t off = f32x2(-8388736.0f, -8388736.0f), s2 = f32x2(s, s);
+#pragma unroll
+  for (uint32_t i = 0; i < 2; ++i) {
+    const uint64_t m = f32x2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540 + 2 * i)),
+                             __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7541 + 2 * i)));
+    const uint64_t x = mul_f32x2(add_f32x2(m, off), s2);
+    v[2 * i] = __uint_as_float(static_cast<uint32_t>(x));
+    v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(x >> 32));
+  }
 }
 
 }  // namespace qnf4

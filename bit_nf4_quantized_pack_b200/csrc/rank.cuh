@@ -107,18 +107,23 @@ struct A8Decoder {
 
   // the codes of k' block kb (zeros from block `end` on and past the matrix)
   __device__ __forceinline__ void fetch(Rows& r, int kb, int end) const {
+    const int row = (kb * kSkW + box) * 64 + kr;
+    const int left = kb < end && col < a8.cols ? a8.rows - row : 0;   // rows from this one on
+    const int8_t* p = a8.codes + static_cast<int64_t>(row) * a8.cols + col + 16 * c;
+    const float* sp = a8.scales + row * bpr + col / 64;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t row = static_cast<int64_t>((kb * kSkW + box) * 64) + kr + 8 * i;
       r.s[i] = 0.0f;
       r.p[i] = make_uint4(0, 0, 0, 0);
-      if (kb < end && row < a8.rows && col < a8.cols) {
+      if (8 * i < left) {
         // volatile asm: the loads issue here, stages before their use
         asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r.p[i].x), "=r"(r.p[i].y), "=r"(r.p[i].z), "=r"(r.p[i].w)
-                     : "l"(a8.codes + row * a8.cols + col + 16 * c));
-        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(r.s[i]) : "l"(a8.scales + row * bpr + col / 64));
+                     : "l"(p));
+        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(r.s[i]) : "l"(sp));
       }
+      p += 8 * static_cast<int64_t>(a8.cols);
+      sp += 8 * bpr;
     }
   }
 
@@ -143,13 +148,12 @@ struct A8Decoder {
     }
   }
 
-  // This turn's K blocks of a tile's kb0 .. kb1 - 1, the first of them the
-  // ring's stage use g0.
+  // This turn's K blocks of kb0 .. kb1 - 1.
   template <typename Wait>
-  __device__ __forceinline__ bool run(int kb0, int kb1, int g0, int turn, uint8_t* sA, uint64_t* full, int lane,
+  __device__ __forceinline__ bool run(int kb0, int kb1, int turn, uint8_t* sA, uint64_t* full, int lane,
                                       Wait&& wait_empty) const {
     Rows r[kSkA8Ahead];
-    const int first = kb0 + ((turn - g0) & (kSkA8Turns - 1));   // stage uses turn, turn + 2, ... are this turn's
+    const int first = kb0 + turn;
 #pragma unroll
     for (int i = 0; i < kSkA8Ahead; ++i) fetch(r[i], first + i * kSkA8Turns, kb1);
     for (int kb = first; kb < kb1; kb += kSkA8Ahead * kSkA8Turns) {
@@ -157,7 +161,7 @@ struct A8Decoder {
       for (int i = 0; i < kSkA8Ahead; ++i) {
         const int k = kb + i * kSkA8Turns;
         if (k < kb1) {
-          const int g = g0 + k - kb0, s = g % kSkStages;
+          const int g = k - kb0, s = g % kSkStages;
           if (!wait_empty(g)) return false;
           store(r[i], sA + s * kSkA);
           fence_proxy_async_smem();
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
     // decoders of the 8-bit operand
     const int t = threadIdx.x - kSkThreads;
     const A8Decoder d(a8, t % (kSkA8Group * 32), m0);
-    if (!d.run(kb0, kb1, 0, t / (kSkA8Group * 32), sA, full, lane,
+    if (!d.run(kb0, kb1, t / (kSkA8Group * 32), sA, full, lane,
                [&](int u) { return mbar_wait(&empty[u % kSkStages], ((u / kSkStages) & 1) ^ 1); }))
       *abort_flag = 1;
   } else if (warp >= 2) {
@@ -382,13 +386,9 @@ __global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
 // one TMEM accumulator (128 x 64 fp32), warps 2..5 read it (released on
 // `tempty` per tile), scale and store.
 // ===========================================================================
-template <bool kAmn, bool kBmn, bool kA8 = false>
-__global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
-    rank_rows_kernel(const __grid_constant__ SkinnyMaps<false, kA8> maps, SkinnyArgs args, SkinnyA8 a8) {
-  static_assert(!kA8 || kAmn, "an 8-bit operand is read transposed");
-  const CUtensorMap* pA = nullptr;
-  const CUtensorMap* pB = &maps.b;
-  if constexpr (!kA8) pA = &maps.a;
+template <bool kAmn, bool kBmn>
+__global__ void __launch_bounds__(kSkThreads, 1)
+    rank_rows_kernel(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB, SkinnyArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSkStages; ++s) {
-      mbar_init(&full[s], kA8 ? 1 + kSkA8Group : 1);
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
@@ -428,8 +428,8 @@ __global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
   pdl_launch_dependents();
 
   if (warp == 0 && lane == 0) {
-    if constexpr (!kA8) tma_prefetch_desc(pA);
-    tma_prefetch_desc(pB);
+    tma_prefetch_desc(&tA);
+    tma_prefetch_desc(&tB);
     int g = 0;   // stage uses over all tiles
     bool ok = true;
     for (int t = blockIdx.x; t < m_tiles && ok; t += gridDim.x) {
@@ -438,24 +438,22 @@ __global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
         const int s = g % kSkStages;
         const uint32_t ph = (g / kSkStages) & 1;
         if (g >= kSkStages && !mbar_wait(&empty[s], ph ^ 1)) { ok = false; break; }
-        mbar_arrive_expect_tx(&full[s], kA8 ? kSkB : kSkA + kSkB);
+        mbar_arrive_expect_tx(&full[s], kSkA + kSkB);
 #pragma unroll
         for (int w = 0; w < kSkW; ++w) {
           const int kx = (i * kSkW + w) * 64;   // boxes past the end arrive as zero fill
           uint8_t* a = sA + s * kSkA + w * 16384;
           uint8_t* b = sB + s * kSkB + w * 8192;
-          if constexpr (!kA8) {
-            if (kAmn) {
-              tma_load_2d(a, pA, &full[s], m0, kx);
-              tma_load_2d(a + 8192, pA, &full[s], m0 + 64, kx);
-            } else {
-              tma_load_2d(a, pA, &full[s], kx, m0);
-            }
+          if (kAmn) {
+            tma_load_2d(a, &tA, &full[s], m0, kx);
+            tma_load_2d(a + 8192, &tA, &full[s], m0 + 64, kx);
+          } else {
+            tma_load_2d(a, &tA, &full[s], kx, m0);
           }
           if (kBmn)
-            tma_load_2d(b, pB, &full[s], 0, kx);
+            tma_load_2d(b, &tB, &full[s], 0, kx);
           else
-            tma_load_2d(b, pB, &full[s], kx, 0);
+            tma_load_2d(b, &tB, &full[s], kx, 0);
         }
       }
     }
@@ -486,17 +484,6 @@ __global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
         umma_commit(&empty[s]);
       }
       umma_commit(done);   // one phase per tile (also drains an aborted tile)
-    }
-    if (!ok) *abort_flag = 1;
-  } else if (kA8 && warp >= 6) {
-    // decoders of the 8-bit operand
-    const int th = threadIdx.x - kSkThreads;
-    int g = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < m_tiles && ok; t += gridDim.x, g += nkb) {
-      const A8Decoder d(a8, th % (kSkA8Group * 32), t * 128);
-      ok = d.run(0, nkb, g, th / (kSkA8Group * 32), sA, full, lane,
-                 [&](int u) { return u < kSkStages || mbar_wait(&empty[u % kSkStages], ((u / kSkStages) & 1) ^ 1); });
     }
     if (!ok) *abort_flag = 1;
   } else if (warp >= 2) {
@@ -665,35 +652,13 @@ cudaError_t run_skinny(const CUtensorMap& ta, const CUtensorMap& tb, int Mp, int
                                                  SkinnySecond{}, SkinnyA8{}, st);
 }
 
-template <bool A, bool B, bool kA8>
+template <bool A, bool B>
 cudaError_t set_rank_rows_attr() {
   static DeviceOnce once;
   return once.run([](int) {
-    return cudaFuncSetAttribute(rank_rows_kernel<A, B, kA8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(rank_rows_kernel<A, B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(kSkSmem));
   });
-}
-
-template <bool A, bool B, bool kA8>
-cudaError_t launch_rank_rows(const SkinnyMaps<false, kA8>& maps, SkinnyArgs a, int Kp, int ctas, SkinnyA8 a8,
-                             cudaStream_t st) {
-  cudaError_t e = set_rank_rows_attr<A, B, kA8>();
-  if (e != cudaSuccess) return e;
-  // at most one CTA per tile, in pairs (a 2 x 1 cluster, so that the SMs left
-  // to the fused GEMM's pairs stay in pairs)
-  const int m_tiles = (a.Mp + 127) / 128;
-  if (ctas > m_tiles) ctas = m_tiles;
-  ctas = (ctas + 1) & ~1;
-  a.nk = (Kp + 64 * kSkW - 1) / (64 * kSkW);
-  a.kb_per_split = a.nk;
-  a.splits = 1;
-  {
-    ProfScope prof(kProfSkinny, st);
-    e = launch_pdl_pair(rank_rows_kernel<A, B, kA8>, dim3(static_cast<unsigned>(ctas)),
-                        dim3(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1, 1), kSkSmem, st, maps, a, a8);
-  }
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
 }
 
 // Pairs of the fused GEMM: the fewest that keep its number of waves of tiles
@@ -736,7 +701,23 @@ cudaError_t run_rank_rows(const CUtensorMap& ta, const CUtensorMap& tb, int Mp, 
   a.out2 = out2;
   a.ld2 = ld2;
   a.d_status = d_status;
-  return launch_rank_rows<kAmn, kBmn, false>(SkinnyMaps<false, false>{ta, tb}, a, Kp, ctas, SkinnyA8{}, st);
+  cudaError_t e = set_rank_rows_attr<kAmn, kBmn>();
+  if (e != cudaSuccess) return e;
+  // at most one CTA per tile, in pairs (a 2 x 1 cluster, so that the SMs left
+  // to the fused GEMM's pairs stay in pairs)
+  const int m_tiles = (a.Mp + 127) / 128;
+  if (ctas > m_tiles) ctas = m_tiles;
+  ctas = (ctas + 1) & ~1;
+  a.nk = (Kp + 64 * kSkW - 1) / (64 * kSkW);
+  a.kb_per_split = a.nk;
+  a.splits = 1;
+  {
+    ProfScope prof(kProfSkinny, st);
+    e = launch_pdl_pair(rank_rows_kernel<kAmn, kBmn>, dim3(static_cast<unsigned>(ctas)), dim3(kSkThreads, 1, 1),
+                        kSkSmem, st, ta, tb, a);
+  }
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
 }
 
 constexpr CUtensorMapDataType kBF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
