@@ -255,15 +255,10 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   }
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // dZ = bf16(c d Bᵀ), both (columns past r are zero: B's rows past r arrive as zero fill)
+  // dX over both weights, after dZ (see below)
   CUtensorMap tG, tU, tBg, tBu;
   if (!make_tmap_2d(&tG, dG, kBF16, 2, M, N, N, 64, 128, kSW128)) return cudaErrorInvalidValue;
   if (!make_tmap_2d(&tU, dU, kBF16, 2, M, N, N, 64, 128, kSW128)) return cudaErrorInvalidValue;
-  if (!make_tmap_2d(&tBg, w.Bg, kBF16, 2, r, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
-  if (!make_tmap_2d(&tBu, w.Bu, kBF16, 2, r, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
-  e = run_skinny_two<false, false>(tG, tBg, tU, tBu, iM, iN, rp, w.c, 0, dZg, dZu, rp, d_status, st, rp);
-  if (e != cudaSuccess) return e;
-  // dX over both weights
   e = set_fused_attr<kModeGatedBwd>();
   if (e != cudaSuccess) return e;
   ModeTypes<kModeGatedBwd>::Maps maps;
@@ -288,6 +283,29 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   ga.packed2 = w.packed_u;
   ga.d_status = d_status;
   set_split(ga, part);
+  // dZ = bf16(c d Bᵀ), both (columns past r are zero: B's rows past r arrive as zero fill)
+  if (!make_tmap_2d(&tBg, w.Bg, kBF16, 2, r, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d(&tBu, w.Bu, kBF16, 2, r, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
+  // On the SMs that dX leaves free, beside it, when they are done before its
+  // first tile comes to the LoRA steps (a CTA there streams about 58 KB a us, and a
+  // K-step takes dX at least 0.55 us); else, and where dX is split (its items
+  // come there soon), over all SMs before it.  The backward so and so: 260 and 269
+  // us at 1500 x 4096 x 11008, 636 and 638 at 4096 x 4096 x 11008, 1004 and 1047 at
+  // 4096 x 5120 x 13824; split, 88 and 86 at 700 x 4096 x 4096.
+  const int free_sms = ga.splits > 1 ? 0 : rank_rows_ctas(0.0, ga.m_tiles * ga.n_tiles, 1.0);
+  const int rounds = free_sms > 0 ? tiles_of(2 * tiles_of(M, 128), free_sms) : 0;
+  if (free_sms > 0 && rounds * 256.0 * N <= 0.032e6 * ga.nk) {
+    SkinnyArgs sa{};
+    sa.Mp = iM;
+    sa.ncols = sa.nout = sa.ld = rp;
+    sa.scale = w.c;
+    sa.out = dZg;
+    sa.d_status = d_status;
+    e = launch_rank_rows<false, false, true>(SkinnyMaps<true, false>{tG, tBg, tU, tBu}, sa, iN, free_sms, dZu, st);
+  } else {
+    e = run_skinny_two<false, false>(tG, tBg, tU, tBu, iM, iN, rp, w.c, 0, dZg, dZu, rp, d_status, st, rp);
+  }
+  if (e != cudaSuccess) return e;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -384,11 +384,12 @@ __global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
 // it start at once and wait for the product only at its LoRA step, and dA,
 // dB here run beside dX.  Same roles as above: warp 0 TMA, warp 1 MMA into
 // one TMEM accumulator (128 x 64 fp32), warps 2..5 read it (released on
-// `tempty` per tile), scale and store.
+// `tempty` per tile), scale and store.  kPair: the tiles of a second product of
+// the same sizes follow those of the first (mode 0 without a copy).
 // ===========================================================================
-template <bool kAmn, bool kBmn>
+template <bool kAmn, bool kBmn, bool kPair>
 __global__ void __launch_bounds__(kSkThreads, 1)
-    rank_rows_kernel(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB, SkinnyArgs args) {
+    rank_rows_kernel(const __grid_constant__ SkinnyMaps<kPair, false> maps, SkinnyArgs args, void* second_out) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(kSkThreads, 1)
   int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int m_tiles = (args.Mp + 127) / 128;
+  const int m_tiles = (args.Mp + 127) / 128, tiles = kPair ? 2 * m_tiles : m_tiles;
   const int nkb = args.nk;
 
   if (threadIdx.x == 0) {
@@ -428,12 +429,20 @@ __global__ void __launch_bounds__(kSkThreads, 1)
   pdl_launch_dependents();
 
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tA);
-    tma_prefetch_desc(&tB);
+    tma_prefetch_desc(&maps.a);
+    tma_prefetch_desc(&maps.b);
     int g = 0;   // stage uses over all tiles
     bool ok = true;
-    for (int t = blockIdx.x; t < m_tiles && ok; t += gridDim.x) {
-      const int m0 = t * 128;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const CUtensorMap *pA = &maps.a, *pB = &maps.b;
+      int m0 = t * 128;
+      if constexpr (kPair) {
+        if (t >= m_tiles) {
+          pA = &maps.a2;
+          pB = &maps.b2;
+          m0 -= m_tiles * 128;
+        }
+      }
       for (int i = 0; i < nkb; ++i, ++g) {
         const int s = g % kSkStages;
         const uint32_t ph = (g / kSkStages) & 1;
@@ -445,15 +454,15 @@ __global__ void __launch_bounds__(kSkThreads, 1)
           uint8_t* a = sA + s * kSkA + w * 16384;
           uint8_t* b = sB + s * kSkB + w * 8192;
           if (kAmn) {
-            tma_load_2d(a, &tA, &full[s], m0, kx);
-            tma_load_2d(a + 8192, &tA, &full[s], m0 + 64, kx);
+            tma_load_2d(a, pA, &full[s], m0, kx);
+            tma_load_2d(a + 8192, pA, &full[s], m0 + 64, kx);
           } else {
-            tma_load_2d(a, &tA, &full[s], kx, m0);
+            tma_load_2d(a, pA, &full[s], kx, m0);
           }
           if (kBmn)
-            tma_load_2d(b, &tB, &full[s], 0, kx);
+            tma_load_2d(b, pB, &full[s], 0, kx);
           else
-            tma_load_2d(b, &tB, &full[s], kx, 0);
+            tma_load_2d(b, pB, &full[s], kx, 0);
         }
       }
     }
@@ -462,7 +471,7 @@ __global__ void __launch_bounds__(kSkThreads, 1)
     constexpr uint32_t idesc = idesc_bf16_f32(128, 64, kAmn ? 1 : 0, kBmn ? 1 : 0);
     int g = 0, it = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < m_tiles && ok; t += gridDim.x, ++it) {
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++it) {
       // the epilogue has read the previous tile's accumulator
       if (it > 0 && !mbar_wait(tempty, (it - 1) & 1)) { ok = false; break; }
       tc_fence_after();
@@ -490,11 +499,13 @@ __global__ void __launch_bounds__(kSkThreads, 1)
     const int q = warp & 3;   // TMEM lanes 32q .. 32q + 31
     const int nc = args.ncols;
     int it = 0;
-    for (int t = blockIdx.x; t < m_tiles; t += gridDim.x, ++it) {
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
       const bool okd = mbar_wait(done, it & 1);
       tc_fence_after();
       if (!okd) { *abort_flag = 1; break; }
-      const int grow = t * 128 + q * 32 + lane;
+      const bool second = kPair && t >= m_tiles;
+      void* const out = second ? second_out : args.out;
+      const int grow = (second ? t - m_tiles : t) * 128 + q * 32 + lane;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         if (c * 32 < nc) {
@@ -502,7 +513,7 @@ __global__ void __launch_bounds__(kSkThreads, 1)
           tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c * 32, v);
           tmem_ld_wait();
           if (grow < args.Mp && args.mode == 0) {
-            uint16_t* o = static_cast<uint16_t*>(args.out) + static_cast<int64_t>(grow) * args.ld;
+            uint16_t* o = static_cast<uint16_t*>(out) + static_cast<int64_t>(grow) * args.ld;
             uint16_t* o2 = args.out2 != nullptr ? args.out2 + static_cast<int64_t>(grow) * args.ld2 : nullptr;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -518,7 +529,7 @@ __global__ void __launch_bounds__(kSkThreads, 1)
           } else if (grow < args.Mp) {
             // fp32: mode 1 out[Mp][ld], mode 2 out[nout][Mp] (consecutive lanes,
             // consecutive rows); mode 3: bf16 out[nout][Mp]
-            float* o = static_cast<float*>(args.out);
+            float* o = static_cast<float*>(out);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int cc = c * 32 + i;
@@ -527,7 +538,7 @@ __global__ void __launch_bounds__(kSkThreads, 1)
                 if (args.mode == 1)
                   o[static_cast<int64_t>(grow) * args.ld + cc] = x;
                 else if (args.mode == 3)
-                  static_cast<uint16_t*>(args.out)[static_cast<int64_t>(cc) * args.Mp + grow] =
+                  static_cast<uint16_t*>(out)[static_cast<int64_t>(cc) * args.Mp + grow] =
                       static_cast<uint16_t>(pack_bf16x2(x, 0.0f) & 0xFFFFu);
                 else
                   o[static_cast<int64_t>(cc) * args.Mp + grow] = x;
@@ -652,11 +663,11 @@ cudaError_t run_skinny(const CUtensorMap& ta, const CUtensorMap& tb, int Mp, int
                                                  SkinnySecond{}, SkinnyA8{}, st);
 }
 
-template <bool A, bool B>
+template <bool A, bool B, bool kPair>
 cudaError_t set_rank_rows_attr() {
   static DeviceOnce once;
   return once.run([](int) {
-    return cudaFuncSetAttribute(rank_rows_kernel<A, B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(rank_rows_kernel<A, B, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(kSkSmem));
   });
 }
@@ -683,6 +694,28 @@ int rank_rows_ctas(double bytes, int tiles, double mb_per_sm) {
   return free_sms;
 }
 
+template <bool kAmn, bool kBmn, bool kPair>
+cudaError_t launch_rank_rows(const SkinnyMaps<kPair, false>& maps, SkinnyArgs a, int Kp, int ctas, void* second_out,
+                             cudaStream_t st) {
+  cudaError_t e = set_rank_rows_attr<kAmn, kBmn, kPair>();
+  if (e != cudaSuccess) return e;
+  // at most one CTA per tile, in pairs (a 2 x 1 cluster, so that the SMs left
+  // to the fused GEMM's pairs stay in pairs)
+  const int tiles = (a.Mp + 127) / 128 * (kPair ? 2 : 1);
+  if (ctas > tiles) ctas = tiles;
+  ctas = (ctas + 1) & ~1;
+  a.nk = (Kp + 64 * kSkW - 1) / (64 * kSkW);
+  a.kb_per_split = a.nk;
+  a.splits = 1;
+  {
+    ProfScope prof(kProfSkinny, st);
+    e = launch_pdl_pair(rank_rows_kernel<kAmn, kBmn, kPair>, dim3(static_cast<unsigned>(ctas)),
+                        dim3(kSkThreads, 1, 1), kSkSmem, st, maps, a, second_out);
+  }
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
 // D = scale * A(m',k') B(n',k') by rank_rows_kernel on `ctas` CTAs; modes as
 // for run_skinny (0: bf16 out, and all ncols columns again into out2 when it
 // is not null; 1: fp32 out[Mp][ld]; 2: fp32 out[nout][Mp]).
@@ -701,23 +734,7 @@ cudaError_t run_rank_rows(const CUtensorMap& ta, const CUtensorMap& tb, int Mp, 
   a.out2 = out2;
   a.ld2 = ld2;
   a.d_status = d_status;
-  cudaError_t e = set_rank_rows_attr<kAmn, kBmn>();
-  if (e != cudaSuccess) return e;
-  // at most one CTA per tile, in pairs (a 2 x 1 cluster, so that the SMs left
-  // to the fused GEMM's pairs stay in pairs)
-  const int m_tiles = (a.Mp + 127) / 128;
-  if (ctas > m_tiles) ctas = m_tiles;
-  ctas = (ctas + 1) & ~1;
-  a.nk = (Kp + 64 * kSkW - 1) / (64 * kSkW);
-  a.kb_per_split = a.nk;
-  a.splits = 1;
-  {
-    ProfScope prof(kProfSkinny, st);
-    e = launch_pdl_pair(rank_rows_kernel<kAmn, kBmn>, dim3(static_cast<unsigned>(ctas)), dim3(kSkThreads, 1, 1),
-                        kSkSmem, st, ta, tb, a);
-  }
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return launch_rank_rows<kAmn, kBmn, false>(SkinnyMaps<false, false>{ta, tb}, a, Kp, ctas, nullptr, st);
 }
 
 constexpr CUtensorMapDataType kBF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
