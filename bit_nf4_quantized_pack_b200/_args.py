@@ -81,7 +81,7 @@ def _buffer(t, dtype, n, name, dev):
 def output(t, like, name, shape, dtype=torch.bfloat16):
     """`t` checked, or a new tensor of `shape` and `dtype` beside `like`."""
     if t is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(*shape, dtype=dtype)   # (a size as one tuple costs half as much again)
     tensor(t, name, shape, like.device, dtype)
     return t
 
@@ -105,7 +105,7 @@ def workspace(given, nbytes, like):
     ordered on the current stream, and under graph capture it belongs to that
     graph's own pool, so no two captured graphs or streams ever share one."""
     if given is None:
-        return like.new_empty((max(nbytes, 256),), dtype=torch.uint8)
+        return like.new_empty(max(nbytes, 256), dtype=torch.uint8)
     dev = like.device
     if (not isinstance(given, torch.Tensor) or given.dtype != torch.uint8 or given.device != dev
             or not given.is_contiguous()):

@@ -54,8 +54,8 @@ def act8_struct(a, name, M, K, dev):
 
 def new_act8(M, K, like):
     """A new Act8 of M x K beside `like`, and its C struct."""
-    codes = like.new_empty((M, K), dtype=torch.int8)
-    scales = like.new_empty((M, K // 64), dtype=torch.float32)
+    codes = like.new_empty(M, K, dtype=torch.int8)
+    scales = like.new_empty(M, K // 64, dtype=torch.float32)
     return Act8(codes, scales), Act8C(M, K, codes.data_ptr(), scales.data_ptr())
 
 

@@ -28,12 +28,50 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 1 / x within a unit in the last place (0 for infinity)
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// two fp32 values an instruction
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ float f32x2_lo(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float f32x2_hi(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // 1 / (1 + exp(-z))
 __device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + ex2(-z * kLog2E)); }
 
-__device__ __forceinline__ float act_value(int act, float g) {
-  const float z = act == QLORA_ACT_SILU ? g : g * fmaf(kGelu2KC * g, g, kGelu2K);
-  return g * logistic(z);
+// act(g) u of two pairs as two bf16, with packed arithmetic: half the
+// instructions (the fused epilogue holds up the products while it runs)
+__device__ __forceinline__ uint32_t act_mul2(int act, float g0, float g1, float u0, float u1) {
+  const uint64_t g = f32x2(g0, g1);
+  uint64_t z = mul_f32x2(g, f32x2(-kLog2E, -kLog2E));
+  if (act != QLORA_ACT_SILU)
+    z = mul_f32x2(z, fma_f32x2(mul_f32x2(g, f32x2(kGelu2KC, kGelu2KC)), g, f32x2(kGelu2K, kGelu2K)));
+  const uint64_t d = add_f32x2(f32x2(ex2(f32x2_lo(z)), ex2(f32x2_hi(z))), f32x2(1.0f, 1.0f));
+  const uint64_t h = mul_f32x2(mul_f32x2(g, f32x2(rcp(f32x2_lo(d)), rcp(f32x2_hi(d)))), f32x2(u0, u1));
+  return pack_bf16x2(f32x2_lo(h), f32x2_hi(h));
 }
 
 // act(g), and its derivative in `d`
@@ -80,26 +118,6 @@ __device__ __forceinline__ float act8_inverse(float s) { return __fdividef(1.0f,
 // values an instruction: the codec is bound by the instructions it issues.
 constexpr float kAct8Magic = 12582912.0f;
 constexpr float kAct8Tiny = 1.0f / (1ull << 50) / (1ull << 50);   // 2^-100
-__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-  return v;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ uint32_t act8_exact(float x, float s) {
   return __float_as_uint(__fadd_rn(rintf(__fdiv_rn(x, s)), kAct8Magic));
 }

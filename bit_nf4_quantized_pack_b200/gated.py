@@ -51,12 +51,12 @@ def _new_saved(M, N, r, save, like):
     """A new GatedSaved beside `like` (a bf16 tensor), and its C struct."""
     if save not in ("bf16", "int8"):
         raise ValueError("save must be None, 'bf16' or 'int8'")
-    zg, zu = like.new_empty((M, r)), like.new_empty((M, r))
+    zg, zu = like.new_empty(M, r), like.new_empty(M, r)
     if save == "int8":
         (g, cg), (u, cu) = new_act8(M, N, like), new_act8(M, N, like)
         return GatedSaved(g, u, zg, zu), GatedSavedC(None, None, cg.codes, cu.codes, cg.scales, cu.scales,
                                                      zg.data_ptr(), zu.data_ptr())
-    g, u = like.new_empty((M, N)), like.new_empty((M, N))
+    g, u = like.new_empty(M, N), like.new_empty(M, N)
     return GatedSaved(g, u, zg, zu), GatedSavedC(g.data_ptr(), u.data_ptr(), None, None, None, None, zg.data_ptr(),
                                                  zu.data_ptr())
 
