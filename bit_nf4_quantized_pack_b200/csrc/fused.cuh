@@ -66,14 +66,15 @@ __constant__ float kNF4g[32] = {QNF4_TABLE_VALUES, QNF4_INT4_VALUES};
 // the stages and signals the accumulators in both CTAs (multicast), and both
 // CTAs' epilogue warps release an accumulator on CTA 0's barrier.
 //
-// After the last K-step of a tile, the LoRA step takes two activation stages:
-// Zc (or dZ) as the activation tile and B (or A) as the weight tile, both by
-// TMA with the rank padded to a multiple of 16 by TMA's zero fill; the decoder
-// warps skip it.  The epilogue releases each accumulator as soon as it has
-// read it, so the next tile's first MMAs overlap the drain of the last; until
-// then they wait for it, so its eight warps only lay their rows out in shared
-// memory, from where TMA stores them (store_rows).  In the backward a warp's TMEM
-// load gives each lane one output column over 32 consecutive rows.
+// After the last K-step of a tile the LoRA step (the gated modes' first before the
+// last two, see lora_early) takes two activation stages: Zc (or dZ) as the
+// activation tile and B (or A) as the weight tile, both by TMA with the rank
+// padded to a multiple of 16 by TMA's zero fill; the decoder warps skip it.  The
+// epilogue releases each accumulator as soon as it has read it, so the next tile's
+// first MMAs overlap the drain of the last; until then they wait for it, so its
+// eight warps only lay their rows out in shared memory, from where TMA stores them
+// (store_rows).  In the backward a warp's TMEM load gives each lane one output
+// column over 32 consecutive rows.
 //
 // Bound: the tensor pipe, 1025 clocks a K-step of a full pair tile (1024 for its
 // products) where the decode keeps up, then the waves of tiles and the power cap.
@@ -387,6 +388,12 @@ __device__ __forceinline__ int tile_rows(const typename ModeTypes<kMode>::Args& 
   else
     return a.rows;
 }
+
+// Whether the first of two LoRA steps goes before the last two K-steps: at the
+// end the second one's tiles would be fetched only once the last K-step has left
+// its stage.  (The gated forward of 1000 x 4096 x 11008: 149.5 us at the end, 147.5 so.)
+template <int kMode>
+__device__ __forceinline__ bool lora_early(int nsteps) { return mode_lora_steps(kMode) > 1 && nsteps >= 4; }
 
 // Slices of 128 rows per CTA of the tile that starts at row m0 which hold rows
 // of the activation (the layer's own modes always run both).
@@ -854,7 +861,42 @@ __global__ void __launch_bounds__(kFThreads, 1)
         // (steps past the contraction's end multiply zeros by zeros: boxes past
         // the end arrive as zero fill, and so do the decoders' rows)
         const int kk0 = split * nsteps;
+        // LoRA step: Zc / dZ into one stage, B / A into the next
+        auto lora = [&](int l) -> bool {
+          if (kLora > 0 && !lora_ready) {
+            pdl_wait();   // Zc (dZ) is the preceding kernel's output
+            lora_ready = true;
+          }
+          const CUtensorMap *la = nullptr, *lb = nullptr;
+          if constexpr (kLora > 0) { la = &maps.la; lb = &maps.lb; }
+          if constexpr (kLora > 1) {
+            if (l == 1) { la = &maps.la2; lb = &maps.lb2; }
+          }
+          uint32_t s1, s2;
+          if (!take(s1, act_bytes)) return false;
+          uint8_t* a = sA + s1 * kFA;
+#pragma unroll
+          for (int h = 0; h < kFSlices; ++h)
+            if (h < nh) tma_load_2d_pair(a + h * 16384, la, bar0(s1), 0, act_row(m0, h));
+          if (!take(s2, kFB)) return false;
+          uint8_t* b = sA + s2 * kFA;
+          if (!kBwd) {
+            // B's columns of this CTA's half, two 64-column boxes (MN-major);
+            // gated: the CTA's own B in its step, rows past the end (zeros) in the other's
+            const int bx = kMode == kModeGatedFwd ? n0 : n0 + 128 * rank;
+            const int by = kMode == kModeGatedFwd && l != rank ? 64 : 0;
+#pragma unroll
+            for (int nb = 0; nb < kFBN / 64; ++nb)
+              tma_load_2d_pair(b + nb * 8192, lb, bar0(s2), bx + nb * 64, by);
+          } else {
+            // A's rows of this CTA's output columns (K-major)
+            tma_load_2d_pair(b, lb, bar0(s2), 0, n0 + 128 * rank);
+          }
+          return true;
+        };
+        const bool early = lora_early<kMode>(nsteps) && split == 0;
         for (int kk = kk0; kk < kk0 + nsteps && ok; ++kk) {
+          if (early && kk == nsteps - 2 && !lora(0)) { ok = false; break; }
           uint32_t s;
           if (!take(s, act_bytes)) { ok = false; break; }
           uint8_t* a = sA + s * kFA;
@@ -871,39 +913,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
             if (h < nh) tma_load_2d_pair(a + h * 16384, ma, bar0(s), kx, act_row(m0, h));
         }
         if (!ok) break;
-        // LoRA steps: Zc / dZ into one stage, B / A into the next
         if (split > 0) continue;
-        if (kLora > 0 && !lora_ready) {
-          pdl_wait();   // Zc (dZ) is the preceding kernel's output
-          lora_ready = true;
-        }
-        for (int l = 0; l < kLora && ok; ++l) {
-          const CUtensorMap *la = nullptr, *lb = nullptr;
-          if constexpr (kLora > 0) { la = &maps.la; lb = &maps.lb; }
-          if constexpr (kLora > 1) {
-            if (l == 1) { la = &maps.la2; lb = &maps.lb2; }
-          }
-          uint32_t s1, s2;
-          if (!take(s1, act_bytes)) { ok = false; break; }
-          uint8_t* a = sA + s1 * kFA;
-#pragma unroll
-          for (int h = 0; h < kFSlices; ++h)
-            if (h < nh) tma_load_2d_pair(a + h * 16384, la, bar0(s1), 0, act_row(m0, h));
-          if (!take(s2, kFB)) { ok = false; break; }
-          uint8_t* b = sA + s2 * kFA;
-          if (!kBwd) {
-            // B's columns of this CTA's half, two 64-column boxes (MN-major);
-            // gated: the CTA's own B in its step, rows past the end (zeros) in the other's
-            const int bx = kMode == kModeGatedFwd ? n0 : n0 + 128 * rank;
-            const int by = kMode == kModeGatedFwd && l != rank ? 64 : 0;
-#pragma unroll
-            for (int nb = 0; nb < kFBN / 64; ++nb)
-              tma_load_2d_pair(b + nb * 8192, lb, bar0(s2), bx + nb * 64, by);
-          } else {
-            // A's rows of this CTA's output columns (K-major)
-            tma_load_2d_pair(b, lb, bar0(s2), 0, n0 + 128 * rank);
-          }
-        }
+        for (int l = early ? 1 : 0; l < kLora && ok; ++l) ok = lora(l);
       }
       if (!ok) *abort_flag = 1;
       // CTA 0: let copies already in flight (its own and the peer's) land
@@ -953,7 +964,27 @@ __global__ void __launch_bounds__(kFThreads, 1)
         const int split = split_of(tile);
         const uint32_t tph = (tc & 1) ^ 1;       // parity of the previous tile's release
         const int nh = tile_slices<kMode>(args, (tile % args.m_tiles) * tile_rows<kMode>(args));
+        auto lora = [&]() -> bool {
+          const uint32_t s1 = sa;
+          if (!wait(&full_a[s1], pha)) return false;
+          next_a();
+          const uint32_t s2 = sa;
+          if (!wait(&full_a[s2], pha)) return false;
+          next_a();
+          tc_fence_after();
+          const uint32_t al = static_cast<uint32_t>(act0) + s1 * (kFA >> 4);
+          const uint32_t wl = static_cast<uint32_t>(lor0) + s2 * (kFA >> 4);
+          for (int j = 0; j < args.rsteps; ++j)
+#pragma unroll
+            for (int h = 0; h < kFSlices; ++h)
+              if (kLayer || h < nh) mma(h, al + j * 2, wl + j * kWSlice, 1u);
+          umma_commit_pair_mc_if(elected, smem_u32(&empty_a[s1]), 0x3);
+          umma_commit_pair_mc_if(elected, smem_u32(&empty_a[s2]), 0x3);
+          return true;
+        };
+        const bool early = lora_early<kMode>(nsteps) && split == 0;
         for (int kk = 0; kk < nsteps; ++kk) {
+          if (early && kk == nsteps - 2 && !lora()) { ok = false; break; }
           if (!wait(&full_a[sa], pha) || !wait(&full_b[sb], phb)) { ok = false; break; }
           tc_fence_after();
           const uint32_t al = static_cast<uint32_t>(act0) + sa * (kFA >> 4);
@@ -988,23 +1019,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
           if (++sb == kFBStages) { sb = 0; phb ^= 1; }
         }
         if (!ok) break;
-        for (int l = 0; l < kLora && split == 0; ++l) {   // LoRA steps
-          const uint32_t s1 = sa;
-          if (!wait(&full_a[s1], pha)) { ok = false; break; }
-          next_a();
-          const uint32_t s2 = sa;
-          if (!wait(&full_a[s2], pha)) { ok = false; break; }
-          next_a();
-          tc_fence_after();
-          const uint32_t al = static_cast<uint32_t>(act0) + s1 * (kFA >> 4);
-          const uint32_t wl = static_cast<uint32_t>(lor0) + s2 * (kFA >> 4);
-          for (int j = 0; j < args.rsteps; ++j)
-#pragma unroll
-            for (int h = 0; h < kFSlices; ++h)
-              if (kLayer || h < nh) mma(h, al + j * 2, wl + j * kWSlice, 1u);
-          umma_commit_pair_mc_if(elected, smem_u32(&empty_a[s1]), 0x3);
-          umma_commit_pair_mc_if(elected, smem_u32(&empty_a[s2]), 0x3);
-        }
+        for (int l = early ? 1 : 0; l < kLora && split == 0 && ok; ++l) ok = lora();
         if (!ok) break;
         umma_commit_pair_mc_if(elected, smem_u32(tfull), 0x3);
       }
