@@ -54,6 +54,30 @@ def test_codec_ties_and_extremes():
     assert np.array_equal(to_np(q.act8_dequantize(a)), oracle.act8_dequantize(codes, scales))
 
 
+def test_codec_over_all_significands_and_magnitudes():
+    """Every pair of significands of a value and its block's largest magnitude, the
+    values up to eight binades below; and blocks through all binades of bf16."""
+    q = _q()
+    sig = np.arange(128, 256) / 128.0
+    values = np.concatenate([sig * 2.0 ** -e for e in range(9)])
+    values = np.resize(np.concatenate([values, -values]), 63 * 37)
+    rows = []
+    for top in sig:
+        block = np.empty((37, 64))
+        block[:, 0] = top
+        block[:, 1:] = values.reshape(37, 63)
+        rows.append(np.where(np.abs(block) <= top, block, 0).reshape(-1))
+    g = np.random.default_rng(3)
+    for e in range(-133, 127, 2):
+        block = g.choice(sig, (37, 64)) * 2.0 ** (e - g.integers(0, 9, (37, 64))) * g.choice([-1, 1], (37, 64))
+        rows.append(block.reshape(-1))
+    x = S.f32_to_bf16_values(np.array(rows).astype(np.float32))
+    a = q.act8_quantize(to_dev(x))
+    codes, scales = oracle.act8_quantize(x)
+    assert np.array_equal(a.scales.cpu().numpy().view(np.uint32), scales.view(np.uint32))
+    assert np.array_equal(a.codes.cpu().numpy(), codes)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_codec_reports_nonfinite(bad):
     q = _q()
