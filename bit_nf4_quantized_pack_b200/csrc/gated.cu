@@ -4,8 +4,8 @@
 //   dG = dH * u * act'(g),  dU = dH * act(g),  dZ = bf16(c·d·Bᵀ),
 //   dX = dG·Ŵgᵀ + dU·Ŵuᵀ + dZg·Agᵀ + dZu·Auᵀ,  dA = Xᵀ·dZ,  dB = Zᵀ·d
 //
-// Forward: the rank-r products of both adapters in one launch, then one fused
-// GEMM over both weights whose epilogue forms H (and keeps g and u, in bf16 or
+// Forward: the rank-r products of both adapters in one launch, before or beside one
+// fused GEMM over both weights whose epilogue forms H (and keeps g and u, in bf16 or
 // in 8 bits).  Backward: one pass over dH, g and u for dG and dU, both dZ in
 // one launch, one fused GEMM over both weights for dX, and beside it both dA
 // and both dB in a launch each.
@@ -105,7 +105,41 @@ cudaError_t run_skinny_two(const CUtensorMap& ta, const CUtensorMap& tb, const C
                                                 SkinnySecond{out_second, pad_second}, SkinnyA8{}, st);
 }
 
+// Two rank-r products X·A or G·Bᵀ on the SMs that the fused GEMM leaves free.
+template <bool kAmn, bool kBmn>
+cudaError_t run_rank_rows_two(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ta2,
+                              const CUtensorMap& tb2, int Mp, int Kp, int ncols, float scale, void* out,
+                              void* out_second, int ld, int ctas, int32_t* d_status, cudaStream_t st, int nout,
+                              uint16_t* pad = nullptr, uint16_t* pad_second = nullptr, int ld2 = 0) {
+  SkinnyArgs a{};
+  a.Mp = Mp;
+  a.ncols = ncols;
+  a.nout = nout;
+  a.scale = scale;
+  a.out = out;
+  a.ld = ld;
+  a.out2 = pad;
+  a.ld2 = ld2;
+  a.d_status = d_status;
+  return launch_rank_rows<kAmn, kBmn, true>(SkinnyMaps<true, false>{ta, tb, ta2, tb2}, a, Kp, ctas,
+                                            SkinnySecond{out_second, pad_second}, st);
+}
+
 int tiles_of(int64_t n, int per) { return static_cast<int>((n + per - 1) / per); }
+
+// SMs that the fused GEMM of `tiles` tiles of `nk` K-steps leaves free, or 0 where
+// two rank-r products over M rows of `cols` columns would not be done there about
+// when its first tile comes to the LoRA steps: a CTA streams about 58 KB a us and
+// loses two at a tile's start and end, a K-step takes 0.55 to 0.75 us.  Against both
+// products split over all SMs before it, the forward: 45.2 and 48.4 us at 333 x 4096 x
+// 4096, 54.5 and 58.7 at 700 x 4096 x 4096, 143 and 149 at 1000 x 4096 x 11008, 199 and
+// 205 at 1500 x 4096 x 11008; beyond the limit 97.4 and 95.2 at 2048 x 2048 x 5632.
+int free_sms_for_two(int64_t M, int64_t cols, int tiles, int nk) {
+  const int sms = rank_rows_ctas(0.0, tiles, 1.0);
+  if (sms == 0) return 0;
+  const int rounds = tiles_of(2 * tiles_of(M, 128), sms);
+  return rounds * (256.0 * cols + 0.1e6) <= 0.037e6 * nk ? sms : 0;
+}
 
 }  // namespace
 
@@ -159,9 +193,6 @@ cudaError_t launch_gated_fwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   if (!make_tmap_2d(&tX, X, kBF16, 2, M, K, K, 64, 128, kSW128)) return cudaErrorInvalidValue;
   if (!make_tmap_2d(&tAg, Ag, kBF16, 2, K, rp, rp, 64, 64, kSW128)) return cudaErrorInvalidValue;
   if (!make_tmap_2d(&tAu, Au, kBF16, 2, K, rp, rp, 64, 64, kSW128)) return cudaErrorInvalidValue;
-  e = run_skinny_two<false, true>(tX, tAg, tX, tAu, iM, iK, rp, w.c, 0, Zg, Zu, keep ? r : rp, d_status, st,
-                                  keep ? r : rp, copy ? Zwg : nullptr, copy ? Zwu : nullptr, rp);
-  if (e != cudaSuccess) return e;
   e = set_fused_attr<kModeGatedFwd>();
   if (e != cudaSuccess) return e;
   ModeTypes<kModeGatedFwd>::Maps maps;
@@ -197,6 +228,18 @@ cudaError_t launch_gated_fwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   ga.Gs = kept.Gs;
   ga.Us = kept.Us;
   ga.d_status = d_status;
+  // Z beside the fused GEMM where it leaves SMs free for long enough, else split
+  // over all SMs before it
+  const int free_sms = free_sms_for_two(M, K, ga.m_tiles * ga.n_tiles, ga.nk);
+  const int zld = keep ? r : rp;
+  uint16_t *pad_g = copy ? Zwg : nullptr, *pad_u = copy ? Zwu : nullptr;
+  if (free_sms > 0)
+    e = run_rank_rows_two<false, true>(tX, tAg, tX, tAu, iM, iK, rp, w.c, Zg, Zu, zld, free_sms, d_status, st, zld,
+                                       pad_g, pad_u, rp);
+  else
+    e = run_skinny_two<false, true>(tX, tAg, tX, tAu, iM, iK, rp, w.c, 0, Zg, Zu, zld, d_status, st, zld, pad_g,
+                                    pad_u, rp);
+  if (e != cudaSuccess) return e;
   const int grid = fused_pairs(ga.m_tiles * ga.n_tiles, num_sms);
   {
     ProfScope prof(kProfGated, st);
@@ -288,25 +331,15 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   // dZ = bf16(c d Bᵀ), both (columns past r are zero: B's rows past r arrive as zero fill)
   if (!make_tmap_2d(&tBg, w.Bg, kBF16, 2, r, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
   if (!make_tmap_2d(&tBu, w.Bu, kBF16, 2, r, N, N, 64, 64, kSW128)) return cudaErrorInvalidValue;
-  // On the SMs that dX leaves free, beside it, when they are done before its
-  // first tile comes to the LoRA steps (a CTA there streams about 58 KB a us, and a
-  // K-step takes dX at least 0.55 us); else, and where dX is split (its items
-  // come there soon), over all SMs before it.  The backward so and so: 260 and 269
-  // us at 1500 x 4096 x 11008, 636 and 638 at 4096 x 4096 x 11008, 1004 and 1047 at
-  // 4096 x 5120 x 13824; split, 88 and 86 at 700 x 4096 x 4096.
-  const int free_sms = ga.splits > 1 ? 0 : rank_rows_ctas(0.0, ga.m_tiles * ga.n_tiles, 1.0);
-  const int rounds = free_sms > 0 ? tiles_of(2 * tiles_of(M, 128), free_sms) : 0;
-  if (free_sms > 0 && rounds * 256.0 * N <= 0.032e6 * ga.nk) {
-    SkinnyArgs sa{};
-    sa.Mp = iM;
-    sa.ncols = sa.nout = sa.ld = rp;
-    sa.scale = w.c;
-    sa.out = dZg;
-    sa.d_status = d_status;
-    e = launch_rank_rows<false, false, true>(SkinnyMaps<true, false>{tG, tBg, tU, tBu}, sa, iN, free_sms, dZu, st);
-  } else {
+  // On the SMs that dX leaves free, beside it, or over all SMs before it; always so
+  // where dX is split (its items come to the LoRA steps soon).  The backward so and
+  // so: 260 and 269 us at 1500 x 4096 x 11008, 632 and 640 at 4096 x 4096 x 11008, 1004
+  // and 1047 at 4096 x 5120 x 13824; split, 88 and 86 at 700 x 4096 x 4096.
+  const int free_sms = ga.splits > 1 ? 0 : free_sms_for_two(M, N, ga.m_tiles * ga.n_tiles, ga.nk);
+  if (free_sms > 0)
+    e = run_rank_rows_two<false, false>(tG, tBg, tU, tBu, iM, iN, rp, w.c, dZg, dZu, rp, free_sms, d_status, st, rp);
+  else
     e = run_skinny_two<false, false>(tG, tBg, tU, tBu, iM, iN, rp, w.c, 0, dZg, dZu, rp, d_status, st, rp);
-  }
   if (e != cudaSuccess) return e;
   int dev = 0;
   cudaGetDevice(&dev);

@@ -385,11 +385,11 @@ __global__ void __launch_bounds__(kSkThreads + (kA8 ? kSkA8Warps * 32 : 0), 1)
 // dB here run beside dX.  Same roles as above: warp 0 TMA, warp 1 MMA into
 // one TMEM accumulator (128 x 64 fp32), warps 2..5 read it (released on
 // `tempty` per tile), scale and store.  kPair: the tiles of a second product of
-// the same sizes follow those of the first (mode 0 without a copy).
+// the same sizes follow those of the first.
 // ===========================================================================
 template <bool kAmn, bool kBmn, bool kPair>
 __global__ void __launch_bounds__(kSkThreads, 1)
-    rank_rows_kernel(const __grid_constant__ SkinnyMaps<kPair, false> maps, SkinnyArgs args, void* second_out) {
+    rank_rows_kernel(const __grid_constant__ SkinnyMaps<kPair, false> maps, SkinnyArgs args, SkinnySecond other) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -504,7 +504,8 @@ __global__ void __launch_bounds__(kSkThreads, 1)
       tc_fence_after();
       if (!okd) { *abort_flag = 1; break; }
       const bool second = kPair && t >= m_tiles;
-      void* const out = second ? second_out : args.out;
+      void* const out = second ? other.out : args.out;
+      uint16_t* const out2 = second ? other.out2 : args.out2;
       const int grow = (second ? t - m_tiles : t) * 128 + q * 32 + lane;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(kSkThreads, 1)
           tmem_ld_wait();
           if (grow < args.Mp && args.mode == 0) {
             uint16_t* o = static_cast<uint16_t*>(out) + static_cast<int64_t>(grow) * args.ld;
-            uint16_t* o2 = args.out2 != nullptr ? args.out2 + static_cast<int64_t>(grow) * args.ld2 : nullptr;
+            uint16_t* o2 = out2 != nullptr ? out2 + static_cast<int64_t>(grow) * args.ld2 : nullptr;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int cc = c * 32 + i;
@@ -695,8 +696,8 @@ int rank_rows_ctas(double bytes, int tiles, double mb_per_sm) {
 }
 
 template <bool kAmn, bool kBmn, bool kPair>
-cudaError_t launch_rank_rows(const SkinnyMaps<kPair, false>& maps, SkinnyArgs a, int Kp, int ctas, void* second_out,
-                             cudaStream_t st) {
+cudaError_t launch_rank_rows(const SkinnyMaps<kPair, false>& maps, SkinnyArgs a, int Kp, int ctas,
+                             SkinnySecond second, cudaStream_t st) {
   cudaError_t e = set_rank_rows_attr<kAmn, kBmn, kPair>();
   if (e != cudaSuccess) return e;
   // at most one CTA per tile, in pairs (a 2 x 1 cluster, so that the SMs left
@@ -710,7 +711,7 @@ cudaError_t launch_rank_rows(const SkinnyMaps<kPair, false>& maps, SkinnyArgs a,
   {
     ProfScope prof(kProfSkinny, st);
     e = launch_pdl_pair(rank_rows_kernel<kAmn, kBmn, kPair>, dim3(static_cast<unsigned>(ctas)),
-                        dim3(kSkThreads, 1, 1), kSkSmem, st, maps, a, second_out);
+                        dim3(kSkThreads, 1, 1), kSkSmem, st, maps, a, second);
   }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
@@ -734,7 +735,7 @@ cudaError_t run_rank_rows(const CUtensorMap& ta, const CUtensorMap& tb, int Mp, 
   a.out2 = out2;
   a.ld2 = ld2;
   a.d_status = d_status;
-  return launch_rank_rows<kAmn, kBmn, false>(SkinnyMaps<false, false>{ta, tb}, a, Kp, ctas, nullptr, st);
+  return launch_rank_rows<kAmn, kBmn, false>(SkinnyMaps<false, false>{ta, tb}, a, Kp, ctas, SkinnySecond{}, st);
 }
 
 constexpr CUtensorMapDataType kBF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
