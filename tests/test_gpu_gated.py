@@ -29,6 +29,10 @@ FORWARD = [  # M, K, N, r, weights, act
     (300, 64, 320, 40, ("dq", "dq"), "silu"),
     (513, 192, 256, 16, ("dq", "dq"), "gelu"),
     (1100, 128, 64, 64, ("dq", "dq"), "silu"),
+    # the rank-r products beside the fused GEMM
+    (300, 1024, 320, 12, ("dq", "absmax"), "silu"),
+    (600, 640, 192, 33, ("dq", "dq"), "gelu"),
+    (1100, 1280, 128, 16, ("int4", "dq"), "silu"),
 ]
 
 
@@ -65,6 +69,7 @@ BACKWARD = [  # M, K, N, r, weights, act, save, gradient type
     (257, 320, 192, 16, ("absmax", "dq"), "silu", "int8", torch.bfloat16),
     (300, 64, 320, 40, ("dq", "dq"), "gelu", "bf16", torch.bfloat16),
     (700, 576, 128, 64, ("dq", "dq"), "silu", "bf16", torch.float32),
+    (1030, 448, 384, 12, ("dq", "dq"), "silu", "int8", torch.float32),
 ]
 
 
