@@ -11,8 +11,8 @@
 // and both dB in a launch each.
 //
 // At 4096 x 4096 x 11008, rank 64, keeping g and u: forward 26 us of rank-r products
-// and 578 of the fused GEMM, backward 83 for dG and dU and about 510 for dX with
-// dZ, dA and dB beside it: 1.44 PFLOP/s in dX, 1.28 in the forward, whose ten waves
+// and 552 of the fused GEMM, backward 83 for dG and dU and about 520 for dX with
+// dZ, dA and dB beside it: 1.44 PFLOP/s in dX, 1.34 in the forward, whose ten waves
 // of tiles hold 9.3.
 #include <mutex>
 
