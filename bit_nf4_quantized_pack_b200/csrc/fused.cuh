@@ -630,6 +630,9 @@ __device__ __forceinline__ void epilogue_loss_grad(const LossArgs& a, const CUte
   const int64_t label = in ? a.labels[row] : -1;
   const bool counts = label_counts(a, row);
   const float lse = in ? a.lse[row] : 0.0f;
+  // once a row: a label that is neither ignored nor in the vocabulary
+  if (a.col0 + n0 + cols == 0 && in && !counts && label != a.ignore_index)
+    raise_status(a.d_status, QLORA_ERR_INVALID_ARG);
 #pragma unroll 1
   for (int c = 0; c < nc; ++c) {
     const int x = n0 + 128 * cols + c * 32;
