@@ -14,8 +14,6 @@
 // and 552 of the fused GEMM, backward 83 for dG and dU and about 520 for dX with
 // dZ, dA and dB beside it: 1.44 PFLOP/s in dX, 1.34 in the forward, whose ten waves
 // of tiles hold 9.3.
-#include <mutex>
-
 #include "act.cuh"
 #include "common.cuh"
 #include "fused.cuh"
@@ -341,8 +339,6 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   else
     e = run_skinny_two<false, false>(tG, tBg, tU, tBu, iM, iN, rp, w.c, 0, dZg, dZu, rp, d_status, st, rp);
   if (e != cudaSuccess) return e;
-  int dev = 0;
-  cudaGetDevice(&dev);
   const int grid = fused_pairs(ga.m_tiles * ga.n_tiles * ga.splits, num_sms);
   // operands of dA and dB, read transposed
   CUtensorMap tXmn, tdZg, tdZu, tGmn, tUmn, tZg, tZu;
@@ -360,11 +356,7 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   // the fork and the join cost more than they hide (the whole step at 333 x 1088
   // x 2752 100 us forked, 89 in order; at 700 x 4096 x 4096 158 and 159; at 1500 x
   // 4096 x 11008 500 and 533).
-  std::lock_guard<std::mutex> lock(g_side_mu);
-  SideStream* ss =
-      prof_timing(kProfSkinny) || !worth_forking(M, K, N) ? nullptr : side_stream(dev);
-  cudaStream_t s2 = st;
-  if (ss != nullptr && cudaEventRecord(ss->fork, st) == cudaSuccess) s2 = ss->s;
+  SideFork fork(st, !prof_timing(kProfSkinny) && worth_forking(M, K, N));
   {
     ProfScope prof(kProfGated, st);
     e = launch_pdl_pair(fused_nf4_gemm_kernel<kModeGatedBwd>, dim3(2 * grid), dim3(kFThreads), kFSmem, st,
@@ -372,13 +364,7 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   }
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e == cudaSuccess && ga.splits > 1) e = launch_split_join(ga, dX, kProfGated, st);
-  if (s2 != st) {
-    const cudaError_t ew = cudaStreamWaitEvent(s2, ss->fork, 0);
-    if (ew != cudaSuccess) {
-      s2 = st;   // no fork: dA and dB after dX on the caller's stream
-      if (e == cudaSuccess) e = ew;
-    }
-  }
+  const cudaStream_t s2 = fork.enter();
   if (e == cudaSuccess && X8 != nullptr) {
     SkinnyArgs sa{};
     sa.Mp = iK;
@@ -397,13 +383,8 @@ cudaError_t launch_gated_bwd(int64_t M, int64_t K, int64_t N, int r, const uint1
   if (e == cudaSuccess)
     e = run_skinny_two<true, true>(tGmn, tZg, tUmn, tZu, iN, iM, r, 1.0f, grad_bf16 ? 3 : 2, dBg, dBu, r,
                                    d_status, s2, r);
-  if (s2 != st) {
-    // always join, so that nothing on st can run ahead of work already queued
-    const cudaError_t ej = cudaEventRecord(ss->join, s2);
-    const cudaError_t ew = ej == cudaSuccess ? cudaStreamWaitEvent(st, ss->join, 0) : ej;
-    if (e == cudaSuccess) e = ew;
-  }
-  return e;
+  const cudaError_t ej = fork.join();
+  return e == cudaSuccess ? ej : e;
 }
 
 }  // namespace qnf4

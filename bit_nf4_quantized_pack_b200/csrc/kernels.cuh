@@ -159,20 +159,32 @@ cudaError_t launch_gemv(int64_t M, int64_t K, int64_t N, int r, const uint16_t* 
                         const uint16_t* B, float c, uint16_t* Y, uint16_t* Zc, int ldz,
                         bool zc_only, int32_t* d_status, cudaStream_t st, int num_sms);
 
-// linear.cu — a library-owned stream per device for work beside the caller's
-// stream (null if it cannot be created).  g_side_mu is held from a fork to its
-// join.
-struct SideStream {
-  cudaStream_t s = nullptr;
-  cudaEvent_t fork = nullptr, join = nullptr;
+// linear.cu — work beside the caller's stream `st`, on a library-owned stream per
+// device: fork, queue on `st` what goes first, enter, queue the work beside it on
+// the stream that enter() gives, join.  That is `st` itself, so that the work runs
+// in order behind the rest, where no fork is wanted or none can be had: no stream
+// could be created, or it is part of a capture that `st` is not part of (a
+// backward captured by another thread takes it in until that capture ends, and a
+// wait across the border would fail and end the capture too).
+struct SideStream;
+class SideFork {
+ public:
+  SideFork(cudaStream_t st, bool wanted);
+  cudaStream_t enter();
+  // `st` waits for the work beside it.  Always called after enter(), so that nothing
+  // on `st` can run ahead of work already queued.
+  cudaError_t join();
+
+ private:
+  std::unique_lock<std::mutex> lock_;   // from the fork to the join: the stream and its events are shared
+  cudaStream_t st_, side_;
+  SideStream* ss_ = nullptr;            // null: in order
 };
-extern std::mutex g_side_mu;
 // Whether a backward's dX (M x K over N) is long enough to run its adapter
 // gradients beside it on that stream.
 inline bool worth_forking(int64_t M, int64_t K, int64_t N) {
   return static_cast<double>(M) * K * N >= 1e10;
 }
-SideStream* side_stream(int dev);
 
 // linear.cu — forward and backward of the layer
 size_t linear_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r);

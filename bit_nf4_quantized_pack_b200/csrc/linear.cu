@@ -37,11 +37,16 @@ namespace qnf4 {
 // (retried after a failure, e.g. inside a stream capture that forbids it);
 // g_side_mu is held from a fork to its join, so concurrent callers never
 // interleave their records and waits on the shared events.
-std::mutex g_side_mu;
+struct SideStream {
+  cudaStream_t s = nullptr;
+  cudaEvent_t fork = nullptr, join = nullptr;
+};
+static std::mutex g_side_mu;
 static SideStream g_side[64];
 
-SideStream* side_stream(int dev) {
-  if (dev < 0 || dev >= 64) return nullptr;
+static SideStream* side_stream() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
   SideStream& ss = g_side[dev];
   if (ss.s == nullptr) {
     int least = 0, greatest = 0;
@@ -61,6 +66,49 @@ SideStream* side_stream(int dev) {
     ss.s = s;
   }
   return &ss;
+}
+
+// Whether work on `side` may depend on work on `st`: `side` is in no capture, or in
+// the one that `st` is in.  (Only a fork takes it into one, under g_side_mu.)
+static bool may_fork(cudaStream_t st, cudaStream_t side) {
+  cudaStreamCaptureStatus a, b;
+  unsigned long long ida = 0, idb = 0;
+  if (cudaStreamGetCaptureInfo(st, &a, &ida) != cudaSuccess ||
+      cudaStreamGetCaptureInfo(side, &b, &idb) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  return b == cudaStreamCaptureStatusNone ||
+         (b == cudaStreamCaptureStatusActive && a == cudaStreamCaptureStatusActive && ida == idb);
+}
+
+SideFork::SideFork(cudaStream_t st, bool wanted) : lock_(g_side_mu), st_(st), side_(st) {
+  SideStream* ss = wanted ? side_stream() : nullptr;
+  if (ss != nullptr && may_fork(st, ss->s)) {
+    if (cudaEventRecord(ss->fork, st) == cudaSuccess)
+      ss_ = ss;
+    else
+      (void)cudaGetLastError();
+  }
+  if (ss_ == nullptr) lock_.unlock();
+}
+
+cudaStream_t SideFork::enter() {
+  if (ss_ != nullptr) {
+    if (cudaStreamWaitEvent(ss_->s, ss_->fork, 0) == cudaSuccess) {
+      side_ = ss_->s;
+    } else {
+      (void)cudaGetLastError();   // in order; what else is wrong shows in the launches
+      ss_ = nullptr;
+    }
+  }
+  return side_;
+}
+
+cudaError_t SideFork::join() {
+  if (ss_ == nullptr) return cudaSuccess;
+  const cudaError_t e = cudaEventRecord(ss_->join, side_);
+  return e == cudaSuccess ? cudaStreamWaitEvent(st_, ss_->join, 0) : e;
 }
 
 size_t linear_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r) {
@@ -278,26 +326,16 @@ cudaError_t launch_linear_bwd(int64_t M, int64_t K, int64_t N, int r, const uint
   // G, on the side stream after dZ, so their CTAs take the SMs that dX's
   // partial last wave of tiles leaves idle.  The caller's stream then waits
   // for them: to the caller the call is ordered as one operation on st.
-  std::lock_guard<std::mutex> lock(g_side_mu);
   // (in order for the smaller backwards of an 8-bit input or with bf16 gradients)
   const bool in_order = (X8 != nullptr || grad_bf16) && !worth_forking(M, K, N);
-  SideStream* ss = prof_timing(kProfSkinny) || in_order ? nullptr : side_stream(dev);
-  cudaStream_t s2 = st;
-  if (ss != nullptr && cudaEventRecord(ss->fork, st) == cudaSuccess) s2 = ss->s;
+  SideFork fork(st, !prof_timing(kProfSkinny) && !in_order);
   {
     ProfScope prof(kProfFusedBwd, st);
     e = launch_pdl_pair(fused_nf4_gemm_kernel<kModeBwd>, dim3(2 * grid), dim3(kFThreads), kFSmem, st,
                         ModeTypes<kModeBwd>::Maps{tG, tdZa, tAl, tdX}, fa);
   }
   if (e == cudaSuccess) e = cudaGetLastError();
-  if (s2 != st) {
-    const cudaError_t ew = cudaStreamWaitEvent(s2, ss->fork, 0);
-    if (ew != cudaSuccess) {
-      // no fork: dA and dB after dX on the caller's stream
-      s2 = st;
-      if (e == cudaSuccess) e = ew;
-    }
-  }
+  const cudaStream_t s2 = fork.enter();
   // dA, dB on the SMs dX leaves free when they can stream their 2 x M x
   // (K + N) bytes there well within dX, else split-K
   const int dx_tiles = fa.m_tiles * fa.n_tiles;
@@ -335,13 +373,8 @@ cudaError_t launch_linear_bwd(int64_t M, int64_t K, int64_t N, int r, const uint
                                        r, Sa, d_status, s2);
     if (e == cudaSuccess) e = run_db();
   }
-  if (s2 != st) {
-    // always join, so that nothing on st can run ahead of work already queued
-    const cudaError_t ej = cudaEventRecord(ss->join, s2);
-    const cudaError_t ew = ej == cudaSuccess ? cudaStreamWaitEvent(st, ss->join, 0) : ej;
-    if (e == cudaSuccess) e = ew;
-  }
-  return e;
+  const cudaError_t ej = fork.join();
+  return e == cudaSuccess ? ej : e;
 }
 
 }  // namespace qnf4
