@@ -43,10 +43,6 @@ class Layer:
     B: torch.Tensor    # r x N_i bf16
     c: float
 
-    @property
-    def widths(self):
-        return self.w.shape
-
 
 @dataclass
 class GatedLayer:
@@ -60,12 +56,12 @@ class GatedLayer:
     c: float
     act: str = "silu"
 
-    @property
-    def widths(self):
-        return self.wg.shape
-
     def args(self):
         return self.wg, self.wu, self.Ag, self.Bg, self.Au, self.Bu, self.c
+
+
+def _widths(layer):
+    return (layer.wg if isinstance(layer, GatedLayer) else layer.w).shape
 
 
 @dataclass
@@ -94,9 +90,9 @@ class LinearChain:
         if policy not in POLICIES:
             raise ValueError("policy must be 'save', 'recompute' or 'int8'")
         for a, b in zip(layers, layers[1:]):
-            if a.widths[1] != b.widths[0]:
+            if _widths(a)[1] != _widths(b)[0]:
                 raise ValueError("layer widths do not chain")
-        if head is not None and layers and layers[-1].widths[1] != head.w.shape[0]:
+        if head is not None and layers and _widths(layers[-1])[1] != head.w.shape[0]:
             raise ValueError("the head's width does not chain")
         self.layers = list(layers)
         self.policy = policy
