@@ -97,7 +97,7 @@ class LinearChain:
         self.layers = list(layers)
         self.policy = policy
         self.head = head
-        self._inputs = []
+        self._inputs = None     # of the last forward
         self._zc = []
 
     def forward(self, X: torch.Tensor, status: torch.Tensor | None = None) -> torch.Tensor:
@@ -120,7 +120,7 @@ class LinearChain:
     def backward(self, dY: torch.Tensor, status: torch.Tensor | None = None):
         """Returns (dX, [the layers' adapter gradients]): (dA_i, dB_i) of a
         linear, (dAg_i, dBg_i, dAu_i, dBu_i) of a gated block."""
-        if not self._inputs:
+        if self._inputs is None:
             raise RuntimeError("backward before forward")
         own = status is None
         status = new_status(dY.device) if own else status
