@@ -28,7 +28,7 @@ import torch
 from . import _args, _lib
 from ._lib import NF4StateC, QLoRAError, check, lib
 from ._status import _finish, new_status, status_clear, status_sync
-from .act8 import Act8, act8_dequantize, act8_quantize, act8_struct
+from .act8 import Act8, act8_dequantize, act8_quantize, act8_struct, width
 from .gated import GatedSaved, gated_backward, gated_forward
 from .loss import head_loss_backward, head_loss_forward
 
@@ -348,7 +348,7 @@ def _linear_backward_act8(dY, X, Zc, w, A, B, c, dX, dA, dB, status, workspace, 
     M, N, dev = _args.cuda_2d(dY, "dY")
     gcode = _args.grad_code(grad_dtype)
     is8 = isinstance(X, Act8)
-    K = X.shape[1] if (is8 or isinstance(X, torch.Tensor)) and len(X.shape) == 2 else -1
+    K = width(X, "X")
     x8 = act8_struct(X, "X", M, K, dev) if is8 else None
     x16 = None if is8 else _args.tensor(X, "X", (M, K), dev)
     if is8 and Zc is None:

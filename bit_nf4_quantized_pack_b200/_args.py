@@ -55,8 +55,18 @@ def tensor(t, name, shape, dev, dtype=torch.bfloat16):
     return t.data_ptr()
 
 
+def columns(w, name):
+    """The columns of an NF4Weight (-1 where it has not two dimensions)."""
+    if not hasattr(w, "packed"):
+        raise TypeError(f"{name} must be an NF4Weight")
+    shape = w.shape
+    return shape[1] if len(shape) == 2 else -1
+
+
 def weight(w, name, K, N, dev):
     """The C struct of an NF4Weight of K x N whose buffers hold what it promises."""
+    if not hasattr(w, "packed"):
+        raise TypeError(f"{name} must be an NF4Weight")
     shape = w.shape
     if len(shape) != 2 or shape[0] != K or shape[1] != N:
         raise ValueError(f"{name} must be {K} x {N}, not {tuple(shape)}")

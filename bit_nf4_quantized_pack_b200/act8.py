@@ -52,6 +52,14 @@ def act8_struct(a, name, M, K, dev):
                  _args.tensor(a.scales, name, (M, K // 64), dev, torch.float32))
 
 
+def width(X, name):
+    """The columns of a matrix or of an Act8 (-1 where it has not two dimensions)."""
+    t = X.codes if isinstance(X, Act8) else X
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a matrix or its Act8")
+    return t.shape[1] if t.dim() == 2 else -1
+
+
 def new_act8(M, K, like):
     """A new Act8 of M x K beside `like`, and its C struct."""
     codes = like.new_empty(M, K, dtype=torch.int8)
@@ -79,7 +87,8 @@ def act8_quantize(X: torch.Tensor, *, out: Act8 | None = None, status: torch.Ten
 
 def act8_dequantize(a: Act8, *, out: torch.Tensor | None = None) -> torch.Tensor:
     """The bf16 matrix that the checkpoint stands for."""
-    if not isinstance(a, Act8) or not a.codes.is_cuda or a.codes.dim() != 2:
+    if (not isinstance(a, Act8) or not isinstance(a.codes, torch.Tensor) or not a.codes.is_cuda
+            or a.codes.dim() != 2):
         raise TypeError("a must be an Act8 on a CUDA device")
     M, K = a.codes.shape
     dev = a.device

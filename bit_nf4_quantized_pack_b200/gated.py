@@ -17,7 +17,7 @@ import torch
 from . import _args
 from ._lib import QLORA_ACT_GELU, QLORA_ACT_SILU, GatedSavedC, check, lib
 from ._status import _finish, new_status
-from .act8 import Act8, act8_struct, new_act8
+from .act8 import Act8, act8_struct, new_act8, width
 
 __all__ = ["GatedSaved", "gated_forward", "gated_backward"]
 
@@ -61,6 +61,12 @@ def _new_saved(M, N, r, save, like):
                                                  zu.data_ptr())
 
 
+def _kept(saved, M, N, r, dev):
+    if not isinstance(saved, GatedSaved):
+        raise TypeError("saved must be a GatedSaved")
+    return saved.cstruct(M, N, r, dev)
+
+
 def _act_code(act):
     if act not in ACTS:
         raise ValueError("act must be 'silu' or 'gelu'")
@@ -69,7 +75,7 @@ def _act_code(act):
 
 def _weights(K, dev, wg, wu, Ag, Bg, Au, Bu):
     """(N, r, the two weights' C structs, the four adapters' addresses)."""
-    N = wg.shape[1] if len(wg.shape) == 2 else -1
+    N = _args.columns(wg, "wg")
     if not isinstance(Ag, torch.Tensor) or Ag.dim() != 2:
         raise TypeError("Ag must be a matrix")
     r = Ag.shape[1]
@@ -94,7 +100,7 @@ def gated_forward(X, wg, wu, Ag, Bg, Au, Bu, c: float, *, act: str = "silu", sav
         H = _args.output(H, X, "H", (M, N))
         kept = None
         if saved is not None:
-            kept = saved.cstruct(M, N, r, dev)
+            kept = _kept(saved, M, N, r, dev)
         elif save is not None:
             saved, kept = _new_saved(M, N, r, save, X)
         ws = _args.workspace(workspace, lib.qlora_gated_fwd_workspace_size(M, K, N, r), X)
@@ -116,15 +122,13 @@ def gated_backward(dH, X, saved: GatedSaved, wg, wu, Ag, Bg, Au, Bu, c: float, *
     M, N, dev = _args.cuda_2d(dH, "dH")
     code, gcode = _act_code(act), _args.grad_code(grad_dtype)
     is8 = isinstance(X, Act8)
-    K = X.shape[1] if (is8 or isinstance(X, torch.Tensor)) and len(X.shape) == 2 else -1
+    K = width(X, "X")
     x8 = act8_struct(X, "X", M, K, dev) if is8 else None
     x16 = None if is8 else _args.tensor(X, "X", (M, K), dev)
     Nw, r, cg, cu, adapters = _weights(K, dev, wg, wu, Ag, Bg, Au, Bu)
     if Nw != N:
         raise ValueError(f"dH must have {Nw} columns, not {N}")
-    if not isinstance(saved, GatedSaved):
-        raise TypeError("saved must be the GatedSaved of the forward")
-    kept = saved.cstruct(M, N, r, dev)
+    kept = _kept(saved, M, N, r, dev)
     with _args.on(dev):
         dX = _args.output(dX, dH, "dX", (M, K))
         dAg = _args.output(dAg, dH, "dAg", (K, r), grad_dtype)

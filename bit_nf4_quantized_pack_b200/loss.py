@@ -19,7 +19,7 @@ __all__ = ["head_loss_forward", "head_loss_backward"]
 
 def _head(X, w, labels, vocab):
     M, K, dev = _args.cuda_2d(X, "X")
-    N = w.shape[1] if len(w.shape) == 2 else -1
+    N = _args.columns(w, "w")
     st = _args.weight(w, "w", K, N, dev)
     y = _args.tensor(labels, "labels", (M,), dev, torch.int64)
     vocab = N if vocab is None else int(vocab)
