@@ -40,9 +40,6 @@ class Act8:
         return Act8(torch.empty((rows, cols), dtype=torch.int8, device=device),
                     torch.empty((rows, cols // 64), dtype=torch.float32, device=device))
 
-    def cstruct(self) -> Act8C:
-        return Act8C(self.codes.shape[0], self.codes.shape[1], self.codes.data_ptr(), self.scales.data_ptr())
-
 
 def act8_struct(a, name, M, K, dev):
     """The C struct of an Act8 of M x K on `dev` with buffers of the right extents."""
