@@ -23,11 +23,12 @@ and its gradients of A carry the checkpoint's rounding.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 
 import torch
 
-from . import (act8_quantize, gated_backward, gated_forward, head_loss_backward, head_loss_forward,
+from . import (_args, act8_quantize, gated_backward, gated_forward, head_loss_backward, head_loss_forward,
                linear_backward, linear_forward, new_status, status_sync)
 from ._lib import QLoRAError
 
@@ -58,6 +59,12 @@ class GatedLayer:
 
     def args(self):
         return self.wg, self.wu, self.Ag, self.Bg, self.Au, self.Bu, self.c
+
+
+def _on(t):
+    """A context in which the tensor's device is current: the layer's calls and the
+    status word's read-back take the current device and its stream."""
+    return _args.on(t.device) if t.is_cuda else contextlib.nullcontext()
 
 
 def _widths(layer):
@@ -101,20 +108,21 @@ class LinearChain:
         self._zc = []
 
     def forward(self, X: torch.Tensor, status: torch.Tensor | None = None) -> torch.Tensor:
-        own = status is None
-        status = new_status(X.device) if own else status
-        self._inputs, self._zc = [], []
-        h = X
-        for L in self.layers:
-            self._inputs.append(act8_quantize(h, status=status) if self.policy == "int8" else h)
-            if isinstance(L, GatedLayer):
-                save = {"save": "bf16", "int8": "int8", "recompute": None}[self.policy]
-                h, kept = gated_forward(h, *L.args(), act=L.act, save=save, status=status)
-            else:
-                h, kept = linear_forward(h, L.w, L.A, L.B, L.c, status=status)
-            self._zc.append(None if self.policy == "recompute" else kept)
-        if own:
-            self._check(status, "forward")
+        with _on(X):
+            own = status is None
+            status = new_status(X.device) if own else status
+            self._inputs, self._zc = [], []
+            h = X
+            for L in self.layers:
+                self._inputs.append(act8_quantize(h, status=status) if self.policy == "int8" else h)
+                if isinstance(L, GatedLayer):
+                    save = {"save": "bf16", "int8": "int8", "recompute": None}[self.policy]
+                    h, kept = gated_forward(h, *L.args(), act=L.act, save=save, status=status)
+                else:
+                    h, kept = linear_forward(h, L.w, L.A, L.B, L.c, status=status)
+                self._zc.append(None if self.policy == "recompute" else kept)
+            if own:
+                self._check(status, "forward")
         return h
 
     def backward(self, dY: torch.Tensor, status: torch.Tensor | None = None):
@@ -122,21 +130,22 @@ class LinearChain:
         linear, (dAg_i, dBg_i, dAu_i, dBu_i) of a gated block."""
         if self._inputs is None:
             raise RuntimeError("backward before forward")
-        own = status is None
-        status = new_status(dY.device) if own else status
-        grads = [None] * len(self.layers)
-        g = dY
-        for i in reversed(range(len(self.layers))):
-            L, x, kept = self.layers[i], self._inputs[i], self._zc[i]
-            if isinstance(L, GatedLayer):
-                if kept is None:
-                    _, kept = gated_forward(x, *L.args(), act=L.act, save="bf16", status=status)
-                g, *d = gated_backward(g, x, kept, *L.args(), act=L.act, status=status)
-            else:
-                g, *d = linear_backward(g, x, kept, L.w, L.A, L.B, L.c, status=status)
-            grads[i] = tuple(d)
-        if own:
-            self._check(status, "backward")
+        with _on(dY):
+            own = status is None
+            status = new_status(dY.device) if own else status
+            grads = [None] * len(self.layers)
+            g = dY
+            for i in reversed(range(len(self.layers))):
+                L, x, kept = self.layers[i], self._inputs[i], self._zc[i]
+                if isinstance(L, GatedLayer):
+                    if kept is None:
+                        _, kept = gated_forward(x, *L.args(), act=L.act, save="bf16", status=status)
+                    g, *d = gated_backward(g, x, kept, *L.args(), act=L.act, status=status)
+                else:
+                    g, *d = linear_backward(g, x, kept, L.w, L.A, L.B, L.c, status=status)
+                grads[i] = tuple(d)
+            if own:
+                self._check(status, "backward")
         return g, grads
 
     def loss_backward(self, X: torch.Tensor, labels: torch.Tensor, status: torch.Tensor | None = None):
@@ -144,13 +153,14 @@ class LinearChain:
         the backward through both.  Returns (mean loss, dX, adapter gradients)."""
         if self.head is None:
             raise RuntimeError("the chain has no head")
-        own = status is None
-        status = new_status(X.device) if own else status
-        h = self.forward(X, status)
-        mean, _, lse = self.head.forward(h, labels, status)
-        dX, grads = self.backward(self.head.backward(h, lse, labels, status), status)
-        if own:
-            self._check(status, "loss_backward")
+        with _on(X):
+            own = status is None
+            status = new_status(X.device) if own else status
+            h = self.forward(X, status)
+            mean, _, lse = self.head.forward(h, labels, status)
+            dX, grads = self.backward(self.head.backward(h, lse, labels, status), status)
+            if own:
+                self._check(status, "loss_backward")
         return mean, dX, grads
 
     @staticmethod
