@@ -124,11 +124,11 @@ class _WorkspaceCache:
 
     CUDA graphs: a captured launch keeps the raw pointer of its workspace.
     While the current stream is capturing, ``get`` never allocates, grows or
-    drops a buffer (a call that needs more than the cached buffer raises: pass
-    ``workspace=`` explicitly, or make the same call once before capturing),
+    drops a buffer (a call that needs more than the cached buffer raises),
     and every buffer handed out during a capture stays referenced for the life
     of the process, so a later, larger call that replaces it cannot hand its
-    memory to another tensor while a graph still writes into it."""
+    memory to another tensor while a graph still writes into it.  The package's
+    own calls do not come here then (``_workspace``)."""
 
     def __init__(self, limit: int = 16):
         self._bufs = {}
@@ -161,6 +161,17 @@ class _WorkspaceCache:
 _ws = _WorkspaceCache()
 
 
+def _workspace(given, key, nbytes, like):
+    """The caller's workspace, or one beside `like`: the cached one of this stream,
+    but a new one while it is capturing, from the capturing graph's own pool.  (Two
+    graphs captured on one stream may be replayed at the same time.)"""
+    if given is not None or nbytes == 0:
+        return given
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    return _ws.get((key, like.device), nbytes, like.device)
+
+
 def quantize(W: torch.Tensor, double_quant: bool = True, *, out: NF4Weight | None = None,
              status: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
              codebook: str = "nf4") -> NF4Weight:
@@ -184,7 +195,7 @@ def quantize(W: torch.Tensor, double_quant: bool = True, *, out: NF4Weight | Non
         raise ValueError("out has another codebook")
     st = w.cstruct()
     need = int(lib.qlora_nf4_quantize_workspace_size(w.numel, st.double_quant))
-    ws = workspace if workspace is not None else _ws.get(("q", W.device), need, W.device)
+    ws = _workspace(workspace, "q", need, W)
     own = status is None
     status = new_status(W.device) if own else status
     check(lib.qlora_nf4_quantize(_ptr(W), dt, C.byref(st), _ptr(ws),
@@ -299,7 +310,7 @@ def linear_forward(X, w: NF4Weight, A, B, c: float, *, Y=None, Zc=None, status=N
     Y = Y if Y is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     Zc = Zc if Zc is not None else torch.empty((M, r), dtype=torch.bfloat16, device=dev)
     need = int(lib.qlora_linear_fwd_workspace_size(M, K, N, r))
-    ws = workspace if workspace is not None else _ws.get(("f", dev), need, dev)
+    ws = _workspace(workspace, "f", need, X)
     st = w.cstruct()
     own = status is None
     status = new_status(dev) if own else status
@@ -330,7 +341,7 @@ def linear_backward(dY, X, Zc, w: NF4Weight, A, B, c: float, *, dX=None, dA=None
     dA = dA if dA is not None else torch.empty((K, r), dtype=torch.float32, device=dev)
     dB = dB if dB is not None else torch.empty((r, N), dtype=torch.float32, device=dev)
     need = int(lib.qlora_linear_bwd_workspace_size(M, K, N, r))
-    ws = workspace if workspace is not None else _ws.get(("b", dev), need, dev)
+    ws = _workspace(workspace, "b", need, X)
     st = w.cstruct()
     own = status is None
     status = new_status(dev) if own else status
