@@ -129,7 +129,8 @@ int tiles_of(int64_t n, int per) { return static_cast<int>((n + per - 1) / per);
 // two rank-r products over M rows of `cols` columns would not be done there about
 // when its first tile comes to the LoRA steps: a CTA streams about 58 KB a us and
 // loses two at a tile's start and end, a K-step takes 0.55 to 0.75 us.  Against both
-// products split over all SMs before it, the forward: 45.2 and 48.4 us at 333 x 4096 x
+// products split over all SMs before it, the forward back to back (alone between
+// other work 1000 x 4096 x 11008 takes 166 us): 45.2 and 48.4 us at 333 x 4096 x
 // 4096, 54.5 and 58.7 at 700 x 4096 x 4096, 143 and 149 at 1000 x 4096 x 11008, 199 and
 // 205 at 1500 x 4096 x 11008; beyond the limit 97.4 and 95.2 at 2048 x 2048 x 5632.
 int free_sms_for_two(int64_t M, int64_t cols, int tiles, int nk) {

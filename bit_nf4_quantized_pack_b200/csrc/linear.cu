@@ -7,15 +7,19 @@
 //
 // Kernels launched from here:
 //   skinny_gemm_kernel   (rank.cuh) rank-r contractions (X·A, G·Bᵀ, Xᵀ·dZ, Gᵀ·Zc): TMA
-//                        for both operands, tcgen05 MMA with N = 64, split-K
-//                        into fp32 partials; the last split of each row
-//                        tile adds them and writes the result.
+//                        for both operands (or a decoded 8-bit X), tcgen05 MMA
+//                        with N = 64, split-K over the CTAs of a cluster, each of
+//                        which adds a share of the rows over all of them through
+//                        distributed shared memory.
+//   rank_rows_kernel     (rank.cuh) the same unsplit, on the SMs that the fused GEMM
+//                        leaves free.
 //   fused_nf4_gemm_kernel  (fused.cuh) Y = X·Ŵ + Zc·B (forward) and dX = G·Ŵᵀ + dZ·Aᵀ
-//                        (backward): persistent, warp-specialised; TMA brings
-//                        activation tiles and packed-nibble tiles, decoder
-//                        warps turn nibbles into bf16 operand tiles in shared
-//                        memory, one thread issues tcgen05.mma into TMEM, and
-//                        the rank-r LoRA term is one extra K-step of the same
+//                        (backward): persistent CTA pairs, warp-specialised; TMA
+//                        brings activation tiles, decoder warps load packed
+//                        nibbles from global memory and turn them into bf16
+//                        operand tiles in shared memory, a converged warp's
+//                        elected lane issues tcgen05.mma into TMEM, and the
+//                        rank-r LoRA term is one extra K-step of the same
 //                        accumulator.
 // The M <= 16 forward (a GEMV) is in gemv.cu.
 #include <atomic>

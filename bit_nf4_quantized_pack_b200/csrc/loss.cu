@@ -11,12 +11,17 @@
 // epilogue writes P = bf16(exp(l - lse) - onehot) (kModeLossGrad); a fused GEMM
 // adds dloss·(P·Ŵᵀ) to the fp32 sums of the pieces before (kModeLossDX).  A
 // piece holds at most about 2^26 elements of P (128 MB): 4096 rows over 32001
-// tokens took 2.76 ms so, 2.90 in pieces of half that (more partial waves of
-// tiles), 2.54 in one piece (which would keep what the logits take).
+// tokens took 5 % longer in pieces of half that (more partial waves of tiles) and
+// 8 % less in one piece (which would keep what the logits take).
 //
-// Bound: the tensor pipe and the power cap.  4096 x 4096 x 32001: statistics 570 us,
-// and per piece of 16128 columns the logits again about 390 and dX 375, 2546 in
-// all (1.27 PFLOP/s); 512 x 8192 x 65536 394 us (1.40).
+// Bound: the tensor pipe and the power cap.  4096 x 4096 x 32001, forward and backward:
+// 2607 us (1.23 PFLOP/s over the three products that run), of which statistics 570
+// and per piece of 16128 columns the logits again about 390 and dX 375; forward
+// alone, 512 x 8192 x 65536, 456 us (1.21).
+// dX splits its contraction where it has few tiles and the vocabulary is one piece.
+// With several pieces it does not: 2048 x 512 over 65536 tokens (two pieces, 8 tiles
+// for 74 pairs) takes 883 us backward beside 205 forward, where 4096 x 4096 over
+// 32001 (128 tiles) takes 1570 beside 723.
 #include "common.cuh"
 #include "fused.cuh"
 #include "kernels.cuh"

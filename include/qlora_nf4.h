@@ -19,12 +19,16 @@
  * - All matrices are dense, row-major and contiguous.  bf16 tensors are passed
  *   as uint16_t bit patterns.  Device pointers must be 16-byte aligned.
  * - Ownership: the caller allocates and frees every buffer, including the
- *   workspace whose size the *_workspace_size functions report.  The library
+ *   workspace whose size the *_workspace_size functions report.  That is the
+ *   size for exactly that shape, and fewer rows can need more (the gated block's
+ *   forward for up to 128 rows, a backward's dX with few tiles): a buffer for
+ *   several row counts takes the largest of their sizes.  The library
  *   never allocates device memory and never synchronizes the stream, except
  *   in qlora_status_sync.
  * - Work is enqueued on `stream` (a cudaStream_t; NULL = legacy default).
- *   qlora_linear_bwd forks part of its work onto a library stream and joins
- *   it back before returning (see there).
+ *   qlora_linear_bwd, qlora_linear_bwd_act8 and qlora_gated_bwd fork part of
+ *   their work onto a library stream and join it back before returning (see
+ *   qlora_linear_bwd).
  * - Errors: a host-side validation failure returns its qlora_status at once and
  *   enqueues nothing.  Errors that only the device can see (non-finite input,
  *   bad padding, an internal wait that ran out) are OR-ed as bit (1 << code)
@@ -305,9 +309,10 @@ qlora_status qlora_linear_fwd(int64_t M, int64_t K, int64_t N, int32_t r,
  * (as in the forward, dZ too runs there when it is small enough).  To the caller the call is still one
  * operation ordered on `stream` (later work on `stream` sees dX, dA and dB;
  * it can be captured in a CUDA graph), and the results are the same bits as
- * a run in order.  If the library stream cannot be created, or while
- * rank-r launches are being timed (qlora_profile_*), everything runs in
- * order on `stream`.
+ * a run in order.  If the library stream cannot be created, while it is part
+ * of a capture that `stream` is not part of (a backward captured on another
+ * stream, until that capture ends), or while rank-r launches are being timed
+ * (qlora_profile_*), everything runs in order on `stream`.
  */
 size_t qlora_linear_bwd_workspace_size(int64_t M, int64_t K, int64_t N, int32_t r);
 qlora_status qlora_linear_bwd(int64_t M, int64_t K, int64_t N, int32_t r,
