@@ -24,7 +24,8 @@
 // the last from the next.)
 //
 // gated_join_kernel adds a column's slots in CTA order (so the result does not
-// depend on timing), forms Z = bf16(c X A) from the last group's slots, adds
+// depend on timing), forms Z = bf16(c X A) from the last group's slots (bf16 as in
+// the layer: the operand that the backward's dB takes), adds
 // Z·B, applies the activation and writes H (and what the backward keeps).
 //
 // Bound: the decode.  A row of 64 weights takes about 217 operations of the pipe
