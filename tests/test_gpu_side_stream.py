@@ -79,10 +79,11 @@ def test_other_stream_and_graph_give_the_same_bits(kind):
         c.check()
 
 
-@pytest.mark.parametrize("captured,eager", [("gated", "linear"), ("linear", "gated"), ("act8", "act8")])
-def test_eager_backward_while_another_stream_is_capturing(captured, eager):
+@pytest.mark.parametrize("captured,eager,default", [("gated", "linear", False), ("linear", "gated", False),
+                                                    ("act8", "act8", False), ("gated", "gated", True)])
+def test_eager_backward_while_another_stream_is_capturing(captured, eager, default):
     a, b = Call(captured, 72), Call(eager, 73)
-    mine, other = torch.cuda.Stream(), torch.cuda.Stream()
+    mine, other = torch.cuda.Stream(), torch.cuda.default_stream() if default else torch.cuda.Stream()
     a.clear()
     b.clear()
     failed = []
